@@ -367,6 +367,136 @@ int kvc_stage_stream_decode(const uint8_t* d_rec, uint32_t rec_bytes, uint32_t n
 int kvc_stage_stream_encode_noalloc(const uint8_t* d_sym, uint32_t n, uint8_t* d_out,
                                     kvc_result* d_res, cudaStream_t stream);
 
+/* ---- Serving cache: the paged, quantised cache a server decodes with, beside
+ * the containers it is exported to. Tokens are quantised as they are written;
+ * token ranges are read back as slices (the layout the encoders take, so a
+ * sequence leaves as a container and a decoded container enters by a write),
+ * and attention reads the codes in place.
+ *
+ * A cache holds n_pages pages of page_tokens tokens. Row (page, kv, head,
+ * token), kv = 0 keys / 1 values, holds head_dim codes and one fp32 scale s;
+ * channel i stands for s * y_i:
+ *   KVC_CACHE_E4M3  y = an 8-bit float (4 exponent, 3 mantissa bits); s = a / 448
+ *   KVC_CACHE_INT8  y = an integer in [-127, 127]; s = a / 127
+ *   KVC_CACHE_E2M1  y = a 4-bit float (0, 0.5, 1, 1.5, 2, 3, 4, 6, signed) times
+ *                   the e4m3 scale u of its block of 16 channels; s = a / 2688
+ * with a the row's largest magnitude. All steps are fp32, rounded to nearest
+ * even: s = a * fl(1 / peak), codes round(x * fl(1 / s)); E2M1: u =
+ * e4m3(m * fl(1 / s) * fl(1 / 6)) with m the block's largest magnitude, codes
+ * e2m1(x * fl(1 / fl(s * u))), zeros where u is. A row with a < 2^-96 is stored
+ * as zeros with s = 0. A row that holds a NaN or an infinity has s = NaN and
+ * zero codes: it reads back as NaN, and so does attention that sees it.
+ *   d_codes   device [n_pages][2][n_heads][page_tokens][row bytes], row bytes =
+ *             head_dim, or head_dim / 2 for E2M1 (channel 2i in the low nibble
+ *             of byte i), 16-byte aligned
+ *   d_scales  device [n_pages][2][n_heads][page_tokens] fp32, 16-byte aligned
+ *   d_micro   E2M1: device [n_pages][2][n_heads][page_tokens][head_dim / 16]
+ *             e4m3 bytes, 16-byte aligned; NULL otherwise
+ * head_dim is 32 .. 256 in steps of 32; page_tokens a power of two, 16 .. 1024.
+ *
+ * Device-side indices (slots, page tables, lengths, starts) are checked on the
+ * device: one that is out of range is not followed, and *d_res (which may be
+ * NULL) gets status KVC_ERR_INVALID. The calls below write d_res->status in
+ * that case only: it stays set until the caller clears it, over any number of
+ * calls, so that a captured step can be checked now and then. */
+enum { KVC_CACHE_E4M3 = 1, KVC_CACHE_INT8 = 2, KVC_CACHE_E2M1 = 3 };
+typedef struct {
+  uint32_t format;
+  uint32_t n_heads, head_dim, page_tokens, n_pages;
+  uint32_t reserved; /* 0 */
+  void* d_codes;
+  float* d_scales;
+  void* d_micro;
+} kvc_cache;
+
+/* Bytes of the three arrays of a cache (its pointers are not looked at; any
+ * out pointer may be NULL). KVC_ERR_INVALID for a bad description. */
+int kvc_cache_bytes(const kvc_cache* cache, size_t* codes, size_t* scales, size_t* micro);
+
+/* Quantise n_tokens tokens and write them to the cache.
+ *   dtype     value type of k and v: KVC_DTYPE_BF16, KVC_DTYPE_FP16, KVC_DTYPE_F32
+ *   d_k, d_v  device values; head h of token t starts at t * token stride + h *
+ *             head stride (in values), channels contiguous. Pointers 16-byte
+ *             aligned and strides multiples of 16 bytes, else KVC_ERR_INVALID.
+ *             Token-major projections and [head][token] slices both fit.
+ *   d_slots   device [n_tokens]: page * page_tokens + token in page; a negative
+ *             slot skips the token (padding). Each slot is given at most once a
+ *             call: of a slot given twice the content is unspecified.
+ * Rows of other slots are left as they are. */
+int kvc_cache_write(const kvc_cache* cache, uint32_t dtype, uint32_t n_tokens, const void* d_k,
+                    int64_t k_token_stride, int64_t k_head_stride, const void* d_v, int64_t v_token_stride,
+                    int64_t v_head_stride, const int64_t* d_slots, kvc_result* d_res, cudaStream_t stream);
+
+/* Read token ranges back: tokens [d_start[b], d_start[b] + n_b) of sequence b,
+ * n_b = d_out_start[b + 1] - d_out_start[b], become tokens [d_out_start[b],
+ * d_out_start[b + 1]) of d_out, device [2][n_heads][out_tokens][head_dim] of
+ * the given dtype (fp32 products s * y rounded to it). Token p of sequence b
+ * lies in page d_pages[b * pages_stride + p / page_tokens].
+ *   d_start      device [n_seqs]
+ *   d_out_start  device [n_seqs + 1], ascending, within [0, out_tokens]
+ * Rows of d_out outside the ranges are left as they are. */
+int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, const int32_t* d_pages,
+                   uint32_t pages_stride, const int32_t* d_start, const int32_t* d_out_start, void* d_out,
+                   uint32_t out_tokens, kvc_result* d_res, cudaStream_t stream);
+
+/* Attention of a batch's newest tokens, softmax(scale * q k^T) v over
+ *   - a prefix that the batch shares (16-bit slices, as a container decodes to
+ *     them), read once for all the sequences' rows together, and
+ *   - each sequence's own tokens in a quantised cache,
+ * either of which may be absent (prefix_tokens = 0; cache = NULL), not both.
+ * Query heads h * g .. h * g + g - 1 (g = n_q_heads / n_heads) read head h.
+ *   dtype          KVC_DTYPE_BF16 or KVC_DTYPE_FP16: q, out and the prefix
+ *   n_rows         query tokens that d_q, d_out and d_lse have room for
+ *   head_dim       64 or 128 (else KVC_ERR_UNSUPPORTED)
+ *   max_queries, max_kv   expected largest number of queries and of cache tokens
+ *                  of a sequence: they size the launch; results do not depend
+ *                  on their being right
+ *   d_q, d_out     device; head h of token t at t * token stride + h * head stride
+ *                  (in values), channels contiguous; 16-byte aligned, strides
+ *                  multiples of 16 bytes
+ *   d_lse          device [n_rows][n_q_heads] fp32 natural log of the sum of
+ *                  exponentials, or NULL
+ *   d_q_start      device [n_seqs + 1], ascending: queries of sequence b are rows
+ *                  d_q_start[b] .. d_q_start[b + 1] - 1; NULL: row b alone
+ *   d_pages, pages_stride   page table, as in kvc_cache_read
+ *   d_kv_len       device [n_seqs]: tokens of sequence b in the cache, its
+ *                  queries' own included: query i of n sees the first
+ *                  d_kv_len[b] - n + i + 1 of them
+ *   d_prefix_k/_v  device [n_heads][prefix_tokens][head_dim], heads
+ *                  prefix_head_stride values apart
+ *   d_prefix_len   device [n_seqs]: how many of the prefix's tokens sequence b
+ *                  sees; NULL: all
+ * A row that sees nothing gets zeros and lse = -infinity. Rows outside
+ * [d_q_start[0], d_q_start[n_seqs]) are left as they are.
+ * kvc_attend_workspace_bytes is the workspace at which the work is split best;
+ * kvc_attend takes any size from kvc_attend_workspace_min up (0 when one part
+ * covers each row) and returns KVC_ERR_CAPACITY below it. d_ws is 16-byte
+ * aligned device memory that no other call uses at the same time; it need not
+ * be initialised. */
+typedef struct {
+  uint32_t dtype, n_rows, n_q_heads, n_heads, head_dim, n_seqs, max_queries, max_kv;
+  float scale;
+  uint32_t prefix_tokens;
+  const void* d_q;
+  int64_t q_token_stride, q_head_stride;
+  void* d_out;
+  int64_t out_token_stride, out_head_stride;
+  float* d_lse;
+  const int32_t* d_q_start;
+  const kvc_cache* cache;
+  const int32_t* d_pages;
+  const int32_t* d_kv_len;
+  uint32_t pages_stride, reserved;
+  const void* d_prefix_k;
+  const void* d_prefix_v;
+  int64_t prefix_head_stride;
+  const int32_t* d_prefix_len;
+} kvc_attend_desc;
+size_t kvc_attend_workspace_bytes(const kvc_attend_desc* desc);
+size_t kvc_attend_workspace_min(const kvc_attend_desc* desc);
+int kvc_attend(const kvc_attend_desc* desc, void* d_ws, size_t ws_bytes, kvc_result* d_res,
+               cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

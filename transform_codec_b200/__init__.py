@@ -26,6 +26,7 @@ BF16, FP16, F32 = 1, 2, 3  # value types (f32: lossless only)
 DTYPE_F32 = F32
 LOSSLESS, TRANSFORM = 0, 1
 ABI_VERSION = 2
+CACHE_E4M3, CACHE_INT8, CACHE_E2M1 = 1, 2, 3  # formats of the quantised serving cache
 RANGES_BLOCK, RANGES_KIVI = 0, 1  # transform value ranges: per block, or KIVI-style per-token values
 
 EXPORTS = [
@@ -39,6 +40,8 @@ EXPORTS = [
     "kvc_profile_begin", "kvc_profile_end",
     "kvc_batch_workspace_bytes", "kvc_encode_batch", "kvc_decode_batch",
     "kvc_stream_buffer_bytes", "kvc_stream_encode_host", "kvc_stream_decode_host",
+    "kvc_cache_bytes", "kvc_cache_write", "kvc_cache_read",
+    "kvc_attend_workspace_bytes", "kvc_attend_workspace_min", "kvc_attend",
 ]
 
 
@@ -70,6 +73,26 @@ class Frame(ctypes.Structure):
                 ("res", ctypes.c_void_p)]
 
 
+class CacheDesc(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_uint32), ("n_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32),
+                ("page_tokens", ctypes.c_uint32), ("n_pages", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("micro", ctypes.c_void_p)]
+
+
+class AttendDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in ("dtype", "n_rows", "n_q_heads", "n_heads", "head_dim", "n_seqs",
+                                               "max_queries", "max_kv")] + [
+        ("scale", ctypes.c_float), ("prefix_tokens", ctypes.c_uint32),
+        ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("cache", ctypes.POINTER(CacheDesc)),
+        ("pages", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("pages_stride", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+        ("prefix_k", ctypes.c_void_p), ("prefix_v", ctypes.c_void_p), ("prefix_head_stride", ctypes.c_int64),
+        ("prefix_len", ctypes.c_void_p),
+    ]
+
+
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 40), ("launches", ctypes.c_uint32),
                 ("total_ms", ctypes.c_double)]
@@ -80,6 +103,8 @@ def _load():
         raise ImportError(f"{LIB_PATH} is missing; build it with transform_codec_b200.build.build()")
     lib = ctypes.CDLL(LIB_PATH)
     vp, sz, u32, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int
+    i64, cache = ctypes.c_int64, ctypes.POINTER(CacheDesc)
+    attend, psz = ctypes.POINTER(AttendDesc), ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "kvc_plan": ([ctypes.POINTER(PlanDesc), ctypes.POINTER(vp)], i32),
         "kvc_plan_create": ([ctypes.POINTER(PlanDesc), ctypes.POINTER(vp)], i32),
@@ -103,6 +128,12 @@ def _load():
         "kvc_stream_buffer_bytes": ([vp, i32, u32], sz),
         "kvc_stream_encode_host": ([vp, i32, u32, u32, u32, vp, vp, sz, vp, vp, vp, sz, vp], i32),
         "kvc_stream_decode_host": ([vp, i32, u32, u32, vp, vp, vp, sz, vp, vp, sz, vp], i32),
+        "kvc_cache_bytes": ([cache, psz, psz, psz], i32),
+        "kvc_cache_write": ([cache, u32, u32, vp, i64, i64, vp, i64, i64, vp, vp, vp], i32),
+        "kvc_cache_read": ([cache, u32, u32, vp, u32, vp, vp, vp, u32, vp, vp], i32),
+        "kvc_attend_workspace_bytes": ([attend], sz),
+        "kvc_attend_workspace_min": ([attend], sz),
+        "kvc_attend": ([attend, vp, sz, vp, vp], i32),
         "kvc_profile_begin": ([], i32),
         "kvc_profile_end": ([ctypes.POINTER(KernelTime), i32, ctypes.POINTER(i32)], i32),
         "kvc_stage_crc32": ([vp, sz, vp, vp], i32),
@@ -382,6 +413,242 @@ def profile_end() -> dict:
     _check(_lib.kvc_profile_end(arr, 64, ctypes.byref(n)), "kvc_profile_end")
     return {arr[i].name.decode(): (int(arr[i].launches), float(arr[i].total_ms))
             for i in range(n.value)}
+
+
+# ---- serving cache
+
+_TORCH_DTYPES: dict = {}
+
+
+def _value_type(dtype) -> int:
+    """BF16, FP16 or F32 of a torch dtype; KvcError (ERR_INVALID) for another."""
+    if not _TORCH_DTYPES:
+        import torch
+        _TORCH_DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: F32})
+    dt = _TORCH_DTYPES.get(dtype)
+    if dt is None:
+        raise KvcError(ERR_INVALID, f"value type {dtype}")
+    return dt
+
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise KvcError(ERR_INVALID, what)
+
+
+def _on(t, device, what: str, dtype=None):
+    """t must be a tensor of that device (and type)."""
+    if t.device != device or (dtype is not None and t.dtype != dtype):
+        raise KvcError(ERR_INVALID, f"{what}: {t.dtype} on {t.device}, not {dtype or ''} on {device}")
+
+
+class _launch_on:
+    """The stream a call launches on, with the tensors' device current."""
+
+    def __init__(self, device, stream):
+        import torch
+        _require(device.type == "cuda", f"tensors on {device}")
+        self._restore = None
+        if torch.cuda.current_device() != device.index:
+            self._restore = torch.cuda.device(device)
+        self._s = torch.cuda.current_stream(device) if stream is None else stream
+
+    def __enter__(self):
+        if self._restore is not None:
+            self._restore.__enter__()
+        return self._s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._restore is not None:
+            self._restore.__exit__(*exc)
+
+
+class QuantCache:
+    """A paged, quantised serving cache of one layer (kvc.h, "Serving cache").
+
+    Owns the arrays codes, scales and micro (E2M1 only), or takes given ones:
+    codes uint8 [n_pages, 2, n_heads, page_tokens, head_dim or head_dim / 2],
+    scales fp32 [n_pages, 2, n_heads, page_tokens], micro uint8 [..., head_dim /
+    16]. res is the sticky kvc_result of the calls on this cache that are not
+    given one: ERR_INVALID once a slot, page or length was out of range."""
+
+    def __init__(self, fmt: int, n_heads: int, head_dim: int, page_tokens: int, n_pages: int, device=None,
+                 codes=None, scales=None, micro=None):
+        import torch
+        self.format, self.n_heads, self.head_dim = fmt, n_heads, head_dim
+        self.page_tokens, self.n_pages = page_tokens, n_pages
+        for v in (fmt, n_heads, head_dim, page_tokens, n_pages):
+            _require(isinstance(v, int) and 0 < v < 1 << 31, "cache shape")
+        self._desc = CacheDesc(fmt, n_heads, head_dim, page_tokens, n_pages, 0, None, None, None)
+        _check(_lib.kvc_cache_bytes(ctypes.byref(self._desc), None, None, None), "kvc_cache_bytes")
+        rows = (n_pages, 2, n_heads, page_tokens)
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        if codes is not None:
+            dev = codes.device
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        four = fmt == CACHE_E2M1
+
+        def array(t, what, dtype, *last):
+            if t is None:
+                return torch.zeros(rows + last, dtype=dtype, device=dev)
+            _on(t, dev, what, dtype)
+            _require(tuple(t.shape) == rows + last and t.is_contiguous(), f"{what} of shape {tuple(t.shape)}")
+            return t
+
+        self.codes = array(codes, "codes", torch.uint8, head_dim // 2 if four else head_dim)
+        self.scales = array(scales, "scales", torch.float32)
+        _require(four or micro is None, "micro-scales of an 8-bit format")
+        self.micro = array(micro, "micro", torch.uint8, head_dim // 16) if four else None
+        self.res = torch.zeros(2, dtype=torch.int64, device=dev)
+        self._desc.codes, self._desc.scales = self.codes.data_ptr(), self.scales.data_ptr()
+        self._desc.micro = self.micro.data_ptr() if four else None
+        self.ref = ctypes.byref(self._desc)
+
+
+def cache_write(cache: QuantCache, k, v, slots, res=None, stream=None):
+    """kvc_cache_write: quantise tokens k, v [n, n_heads, head_dim] (bf16, fp16
+    or f32; token and head strides free in 16-byte steps, so [head][token]
+    slices go in as slices.transpose(0, 1)) into slots, int64 [n] = page *
+    page_tokens + token in page, negative: skipped. Each slot at most once a call."""
+    import torch
+    shape = (slots.shape[0], cache.n_heads, cache.head_dim)
+    _require(k.shape == shape and v.shape == shape, f"k {tuple(k.shape)}, v {tuple(v.shape)} for {shape}")
+    _on(k, cache.device, "k")
+    _on(v, cache.device, "v", k.dtype)
+    _on(slots, cache.device, "slots", torch.int64)
+    kt, kh, kc = k.stride()
+    vt, vh, vc = v.stride()
+    _require(kc == 1 and vc == 1 and slots.is_contiguous(), "channels and slots are contiguous")
+    with _launch_on(cache.device, stream) as s:
+        _check(_lib.kvc_cache_write(cache.ref, _value_type(k.dtype), shape[0], k.data_ptr(), kt, kh, v.data_ptr(),
+                                    vt, vh, slots.data_ptr(), (cache.res if res is None else res).data_ptr(), s),
+               "kvc_cache_write")
+
+
+def cache_read(cache: QuantCache, page_table, start, out_start, out, res=None, stream=None):
+    """kvc_cache_read: tokens [start[b], start[b] + n_b) of each sequence into
+    out [2, n_heads, out_tokens, head_dim] (bf16, fp16 or f32, contiguous: with one
+    sequence the slices the codec takes) at out_start[b] .. out_start[b + 1].
+    page_table int32 [n_seqs, pages], start int32 [n_seqs], out_start int32
+    [n_seqs + 1]; tokens of out outside the ranges are left as they are."""
+    import torch
+    for t, what in ((page_table, "page_table"), (start, "start"), (out_start, "out_start")):
+        _on(t, cache.device, what, torch.int32)
+    _on(out, cache.device, "out")
+    n = start.shape[0]
+    _require(page_table.dim() == 2 and page_table.shape[0] == n and out_start.shape == (n + 1,) and start.dim() == 1,
+             "page_table [n], start [n] and out_start [n + 1]")
+    _require(out.dim() == 4 and out.shape[0] == 2 and out.shape[1] == cache.n_heads
+             and out.shape[3] == cache.head_dim, f"out of shape {tuple(out.shape)}")
+    _require(page_table.is_contiguous() and start.is_contiguous() and out_start.is_contiguous()
+             and out.is_contiguous(), "contiguous tensors")
+    with _launch_on(cache.device, stream) as s:
+        _check(_lib.kvc_cache_read(cache.ref, _value_type(out.dtype), n, page_table.data_ptr(), page_table.shape[1],
+                                   start.data_ptr(), out_start.data_ptr(), out.data_ptr(), out.shape[2],
+                                   (cache.res if res is None else res).data_ptr(), s), "kvc_cache_read")
+
+
+class Attention:
+    """kvc_attend for batches up to a size: owns the workspace (one call at a
+    time) and a sticky kvc_result, res, for calls without one.
+
+    dtype (torch.bfloat16 or torch.float16) is that of q, out and the prefix;
+    max_rows query tokens in all, max_seqs sequences, max_queries and max_kv the
+    expected most of one sequence, prefix_tokens the longest shared prefix. Runs
+    may be smaller; larger ones are refused with ERR_CAPACITY where the
+    workspace does not do."""
+
+    def __init__(self, dtype, n_q_heads: int, n_heads: int, head_dim: int, max_rows: int, max_seqs: int,
+                 max_queries: int = 1, max_kv: int = 0, prefix_tokens: int = 0, device=None):
+        import torch
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.dtype = dev, dtype
+        d = self._desc = AttendDesc()
+        d.dtype, d.n_q_heads, d.n_heads, d.head_dim = _value_type(dtype), n_q_heads, n_heads, head_dim
+        d.n_rows, d.n_seqs, d.max_queries, d.max_kv = max_rows, max_seqs, max_queries, max_kv
+        d.prefix_tokens, d.scale = prefix_tokens, 1.0
+        # any format and page size: the workspace does not depend on them
+        shape = CacheDesc(CACHE_E4M3, n_heads, head_dim, 16, 1, 0, None, None, None)
+        d.cache = ctypes.pointer(shape)
+        self._probe(d)
+        self.workspace = torch.empty(max(_lib.kvc_attend_workspace_bytes(ctypes.byref(d)), 16), dtype=torch.uint8,
+                                     device=dev)
+        self.res = torch.zeros(2, dtype=torch.int64, device=dev)
+        self._ws, self._ws_bytes = self.workspace.data_ptr(), self.workspace.numel()
+        self._ref = ctypes.byref(d)
+
+    @staticmethod
+    def _probe(d):
+        """The status of a bad description: the sizing calls answer 0 for one."""
+        _require(d.n_heads > 0 and d.n_q_heads > 0 and d.n_q_heads % d.n_heads == 0, "query heads for each head")
+        if d.head_dim not in (64, 128):
+            raise KvcError(ERR_UNSUPPORTED, f"head_dim {d.head_dim}")
+        _require(d.dtype in (BF16, FP16), "attention value type")
+
+    def run(self, q, out, cache: QuantCache | None = None, page_table=None, kv_len=None, q_start=None, prefix=None,
+            prefix_len=None, lse=None, scale: float | None = None, res=None, stream=None):
+        """q, out [n, n_q_heads, head_dim] (token and head strides free in 16-byte
+        steps); cache with page_table int32 [n_seqs, pages] and kv_len int32
+        [n_seqs]; q_start int32 [n_seqs + 1] (None: one query a sequence); prefix
+        (k, v), each [n_heads, tokens, head_dim], tokens contiguous; prefix_len
+        int32 [n_seqs] (None: all of it); lse fp32 [n, n_q_heads]; scale defaults
+        to head_dim ** -0.5."""
+        import torch
+        d, dev = self._desc, self.device
+        n, heads, dim = q.shape
+        _on(q, dev, "q", self.dtype)
+        _on(out, dev, "out", self.dtype)
+        _require(heads == d.n_q_heads and dim == d.head_dim and out.shape == q.shape, f"q {tuple(q.shape)}")
+        qs, os_ = q.stride(), out.stride()
+        _require(qs[2] == 1 and os_[2] == 1, "channels are contiguous")
+        seqs = None
+        for t, what, extra in ((q_start, "q_start", 1), (kv_len, "kv_len", 0), (prefix_len, "prefix_len", 0)):
+            if t is not None:
+                _on(t, dev, what, torch.int32)
+                _require(t.dim() == 1 and t.is_contiguous(), what)
+                m = t.shape[0] - extra
+                _require(m >= 0 and (seqs is None or seqs == m), f"{what} for {m} sequences")
+                seqs = m
+        d.n_rows, d.n_seqs = n, n if seqs is None else seqs
+        _require(q_start is not None or n >= d.n_seqs, "a row for each sequence")
+        d.q, d.q_token_stride, d.q_head_stride = q.data_ptr(), qs[0], qs[1]
+        d.out, d.out_token_stride, d.out_head_stride = out.data_ptr(), os_[0], os_[1]
+        d.q_start = None if q_start is None else q_start.data_ptr()
+        d.prefix_len = None if prefix_len is None else prefix_len.data_ptr()
+        d.scale = dim ** -0.5 if scale is None else scale
+        if lse is None:
+            d.lse = None
+        else:
+            _on(lse, dev, "lse", torch.float32)
+            _require(lse.shape == (n, heads) and lse.is_contiguous(), f"lse {tuple(lse.shape)}")
+            d.lse = lse.data_ptr()
+        if cache is None:
+            d.cache, d.pages, d.kv_len = None, None, None
+        else:
+            _require(cache.device == dev and page_table is not None and kv_len is not None, "cache")
+            _on(page_table, dev, "page_table", torch.int32)
+            _require(page_table.dim() == 2 and page_table.shape[0] == d.n_seqs and page_table.is_contiguous(),
+                     "page_table")
+            d.cache = ctypes.pointer(cache._desc)
+            d.pages, d.pages_stride, d.kv_len = page_table.data_ptr(), page_table.shape[1], kv_len.data_ptr()
+        if prefix is None:
+            d.prefix_tokens = 0
+        else:
+            pk, pv = prefix
+            _on(pk, dev, "prefix keys", self.dtype)
+            _on(pv, dev, "prefix values", self.dtype)
+            st = pk.stride()
+            _require(pk.dim() == 3 and pk.shape[0] == d.n_heads and pk.shape[2] == dim and pv.shape == pk.shape
+                     and st[1:] == (dim, 1) and (pv.stride() == st), f"prefix {tuple(pk.shape)}")
+            d.prefix_tokens, d.prefix_head_stride = pk.shape[1], st[0]
+            d.prefix_k, d.prefix_v = pk.data_ptr(), pv.data_ptr()
+        with _launch_on(dev, stream) as s:
+            _check(_lib.kvc_attend(self._ref, self._ws, self._ws_bytes, (self.res if res is None else res).data_ptr(),
+                                   s), "kvc_attend")
 
 
 def stage_crc32(src, n: int, out, stream=None):

@@ -11,8 +11,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkvc.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
-SOURCES = ["api.cpp", "container.cu", "lossless.cu", "transform.cu"]
-HEADERS = ["kvc_device.cuh", "kvc_internal.h", "tcgen05.cuh"]
+SOURCES = ["api.cpp", "serving.cpp", "container.cu", "lossless.cu", "transform.cu", "cache.cu", "attend.cu"]
+HEADERS = ["kvc_device.cuh", "kvc_internal.h", "tcgen05.cuh", "serving.h", "cache_codes.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
