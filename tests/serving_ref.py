@@ -97,15 +97,17 @@ class HostCache:
         return kvc.QuantCache(self.fmt, self.heads, self.dim, self.page, self.codes.shape[0], codes=self.codes.cuda(),
                               scales=self.scales.cuda(), micro=None if self.micro is None else self.micro.cuda())
 
-    def values(self, b, n=None):
-        """fp64 [2][heads][n][dim] of sequence b's first n tokens."""
-        n = self.lens[b] if n is None else n
-        pos = torch.arange(n)
+    def values(self, b, parts=False):
+        """fp64 [2][heads][n][dim] of sequence b's tokens; parts: code values and scales [2][heads][n] instead."""
+        pos = torch.arange(self.lens[b])
         page = self.table[b].long()[pos // self.page]
         at = pos % self.page
         micro = None if self.micro is None else self.micro[page, :, :, at]
         y = code_values(self.fmt, self.codes[page, :, :, at], micro)
-        return (y * self.scales[page, :, :, at].double()[..., None]).permute(1, 2, 0, 3)
+        scale = self.scales[page, :, :, at].double()
+        if parts:
+            return y.permute(1, 2, 0, 3), scale.permute(1, 2, 0)
+        return (y * scale[..., None]).permute(1, 2, 0, 3)
 
 
 def attention(q, starts, host=None, prefix=None, prefix_len=None, scale=1.0):
@@ -113,8 +115,9 @@ def attention(q, starts, host=None, prefix=None, prefix_len=None, scale=1.0):
     to its type, for q [n][Hq][D] (CPU, 16-bit): out, lse and (bounds of out, bounds of lse).
 
     Roundings: weights enter the second product in 16 bits, off by at most u_p =
-    2^-8 (bf16) or 2^-11 (fp16) of themselves, or, as fp16 next to a largest
-    weight of 1 or more, by 2^-25; scores are fp32 sums of D products, each
+    2^-8 (bf16) or 2^-11 (fp16) of themselves, or by half of fp16's smallest step,
+    2^-25, where the largest weight is 2^7 or more (a weight of a cache token
+    holds its value scale; the codes are the other factor); scores are fp32 sums of D products, each
     partial sum off by 2^-23 of the sum of magnitudes at most (truncating adders
     included), which moves a weight by that much relative to itself, twice
     (itself and the sum); q as fp16 next to its largest element of 2^7 or more
@@ -138,6 +141,9 @@ def attention(q, starts, host=None, prefix=None, prefix_len=None, scale=1.0):
             k = torch.cat((prefix[0][:, :p].double(), k), 1)
             v = torch.cat((prefix[1][:, :p].double(), v), 1)
         own = kv.shape[2]
+        if own:
+            codes, scales = host.values(b, parts=True)
+            y, sv = codes[1], scales[1]
         for i in range(m):
             sees = p + max(0, own - m + i + 1)
             if not sees:
@@ -151,7 +157,10 @@ def attention(q, starts, host=None, prefix=None, prefix_len=None, scale=1.0):
             out[first + i] = (w @ v[:, :sees]).reshape(Hq, D)
             weight = w @ v[:, :sees].abs()
             step = 2.0 ** -23 * (D + 8) * mag.amax(-1, keepdim=True)
-            low = 2.0 ** -25 * w.amax(-1, keepdim=True) * v[:, :sees].abs().sum(1)[:, None]
+            low = 2.0 ** -32 * w[..., :p].amax(-1, keepdim=True) * v[:, :p].abs().sum(1)[:, None] if p else 0.0
+            if sees > p:
+                biggest = (w[..., p:] * sv[:, None, :sees - p]).amax(-1, keepdim=True)
+                low = low + 2.0 ** -32 * biggest * y[:, :sees - p].abs().sum(1)[:, None]
             ltol[first + i] = (step + 2.0 ** -18 + 2.0 ** -23 * l.abs()[..., None]).reshape(Hq)
             tol[first + i] = ((u_p + 2 * step + 2.0 ** -18) * weight + low).reshape(Hq, D)
     return out, lse, (tol, ltol)

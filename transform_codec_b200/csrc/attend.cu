@@ -1,52 +1,23 @@
 // Attention over the serving cache and a shared prefix (include/kvc.h,
-// kvc_attend). One block per query row and head: its warps take every fourth
-// token of the prefix and of the sequence's cache, each with a running maximum
-// and sum, and are joined at the end.
-#include "cache_codes.cuh"
-#include "serving.h"
+// kvc_attend): launches, the division of work into parts, and their join.
+#include "attend_cache.cuh"
+#include "attend_parts.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr uint32_t kWarps = 4;
-
-struct RowPlace {
-  int32_t seq, first, last;  // sequence (-1: none) and its rows
-};
-__device__ inline RowPlace place_of(const AttendArgs& a, int32_t i) {
-  if (!a.q_start) return {i < int32_t(a.n_seqs) ? i : -1, i, i + 1};
-  uint32_t lo = 0, hi = a.n_seqs - 1;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.q_start + mid) <= i) lo = mid; else hi = mid - 1;
-  }
-  const int32_t first = __ldg(a.q_start + lo), last = __ldg(a.q_start + lo + 1);
-  if (i < first || i >= last) return {-1, 0, 0};
-  if (first < 0 || last > int32_t(a.n_rows)) {
-    flag_invalid(a.res);
-    return {-1, 0, 0};
-  }
-  return {int32_t(lo), first, last};
-}
-
-__device__ inline float code_value(const CacheView& c, uint64_t row, uint32_t ch) {
-  const uint8_t* p = c.codes + row * c.row_bytes;
-  if (c.fmt == KVC_CACHE_E4M3) return e4m3_f32(p[ch]);
-  if (c.fmt == KVC_CACHE_INT8) return float(int8_t(p[ch]));
-  const float2 f = half2_f32(e2m1x2_half2(p[ch >> 1]));
-  return (ch & 1 ? f.y : f.x) * e4m3_f32(c.micro[row * (c.D / 16u) + ch / 16u]);
-}
+// Prefix: one block per query row and head, for now.
+constexpr uint32_t kRowWarps = 4;
 __device__ inline float value16(uint32_t dtype, const void* p, int64_t at) {
   const uint32_t w = static_cast<const uint16_t*>(p)[at];
   return dtype == KVC_DTYPE_BF16 ? bf16_lo(w) : half2_f32(w).x;
 }
-
-template <uint32_t NC>  // channels a lane
-__global__ void __launch_bounds__(kWarps * 32) k_attend_rows(const AttendArgs a, const CacheView c) {
+template <uint32_t NC>
+__global__ void __launch_bounds__(kRowWarps * 32) k_attend_prefix_rows(const AttendArgs a, const PartsView parts) {
   const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int32_t i = int32_t(blockIdx.x);
   const uint32_t hq = blockIdx.y, h = hq / a.G;
-  const RowPlace at = place_of(a, i);
+  const RowPlace at = place_of_row(a, i);
   if (at.seq < 0) return;
   float q[NC], acc[NC], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -54,59 +25,21 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_rows(const AttendArgs a,
     q[j] = value16(a.dtype, a.q, i * a.q_tok + hq * a.q_head + lane * NC + j) * a.scale_log2;
     acc[j] = 0.f;
   }
-  auto step = [&](const float* k, const float* v) {
+  const int32_t n = int32_t(prefix_seen(a, at.seq));
+  for (int32_t t = int32_t(warp); t < n; t += kRowWarps) {
+    const int64_t off = h * a.p_head + int64_t(t) * a.D + lane * NC;
     float s = 0.f;
 #pragma unroll
-    for (uint32_t j = 0; j < NC; ++j) s = fmaf(q[j], k[j], s);
+    for (uint32_t j = 0; j < NC; ++j) s = fmaf(q[j], value16(a.dtype, a.pk, off + j), s);
     for (uint32_t o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float m2 = s > m ? s : m;
-    const float f = m2 == m ? 1.f : exp2f(m - m2), p = m2 == -INFINITY ? (s == s ? 0.f : s) : exp2f(s - m2);
+    const float f = m2 == m ? 1.f : exp2f(m - m2), p = exp2f(s - m2);
     l = fmaf(l, f, p);
 #pragma unroll
-    for (uint32_t j = 0; j < NC; ++j) acc[j] = fmaf(acc[j], f, p * v[j]);
+    for (uint32_t j = 0; j < NC; ++j) acc[j] = fmaf(acc[j], f, p * value16(a.dtype, a.pv, off + j));
     m = m2;
-  };
-  float k[NC], v[NC];
-  if (a.prefix_tokens) {
-    int32_t n = int32_t(a.prefix_tokens);
-    if (a.prefix_len) {
-      const int32_t w = __ldg(a.prefix_len + at.seq);
-      if (w < 0 || w > n) flag_invalid(a.res);
-      n = max(0, min(w, n));
-    }
-    for (int32_t t = int32_t(warp); t < n; t += kWarps) {
-      const int64_t o = h * a.p_head + int64_t(t) * a.D + lane * NC;
-#pragma unroll
-      for (uint32_t j = 0; j < NC; ++j) {
-        k[j] = value16(a.dtype, a.pk, o + j);
-        v[j] = value16(a.dtype, a.pv, o + j);
-      }
-      step(k, v);
-    }
   }
-  if (a.has_cache) {
-    int64_t len = __ldg(a.kv_len + at.seq);
-    const int64_t room = int64_t(a.pages_stride) << c.page_shift;
-    if (len < 0 || len > room) flag_invalid(a.res);
-    len = max(int64_t(0), min(len, room));
-    const int64_t sees = len - (at.last - at.first) + (i - at.first) + 1;
-    for (int64_t t = warp; t < sees; t += kWarps) {
-      const int32_t page = __ldg(a.pages + uint64_t(at.seq) * a.pages_stride + (t >> c.page_shift));
-      if (page < 0 || uint32_t(page) >= c.n_pages) {
-        flag_invalid(a.res);
-        continue;
-      }
-      const uint64_t rk = cache_row(c, page, 0, h) + (t & c.page_mask), rv = cache_row(c, page, 1, h) + (t & c.page_mask);
-      const float sk = c.scales[rk], sv = c.scales[rv];
-#pragma unroll
-      for (uint32_t j = 0; j < NC; ++j) {
-        k[j] = code_value(c, rk, lane * NC + j) * sk;
-        v[j] = code_value(c, rv, lane * NC + j) * sv;
-      }
-      step(k, v);
-    }
-  }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][NC * 32];
+  __shared__ float sm[kRowWarps], sl[kRowWarps], so[kRowWarps][NC * 32];
   if (lane == 0) {
     sm[warp] = m;
     sl[warp] = l;
@@ -116,38 +49,173 @@ __global__ void __launch_bounds__(kWarps * 32) k_attend_rows(const AttendArgs a,
   __syncthreads();
   if (warp) return;
   float top = -INFINITY, sum = 0.f;
-  for (uint32_t w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
+  for (uint32_t w = 0; w < kRowWarps; ++w) top = fmaxf(top, sm[w]);
 #pragma unroll
   for (uint32_t j = 0; j < NC; ++j) acc[j] = 0.f;
-  for (uint32_t w = 0; w < kWarps; ++w) {
-    const float f = sm[w] == -INFINITY ? (sl[w] == 0.f ? 0.f : NAN) : exp2f(sm[w] - top);
+  for (uint32_t w = 0; w < kRowWarps; ++w) {
+    const float f = sl[w] == 0.f ? 0.f : exp2f(sm[w] - top);
     sum = fmaf(sl[w], f, sum);
     for (uint32_t j = 0; j < NC; ++j) acc[j] = fmaf(so[w][lane * NC + j], f, acc[j]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (uint32_t j = 0; j < NC; ++j) {
-    const float y = acc[j] * inv;
-    const int64_t o = i * a.o_tok + hq * a.o_head + lane * NC + j;
-    static_cast<uint16_t*>(a.out)[o] =
-        uint16_t(a.dtype == KVC_DTYPE_BF16 ? pack_bf16(y, y) : pack_half(y, y));
+  const uint64_t id = uint64_t(i) * a.Hq + hq;
+  for (uint32_t j = 0; j < NC; ++j) parts.o[id * a.D + lane * NC + j] = acc[j] * inv;
+  if (lane == 0) parts.lse[id] = sum == 0.f ? -INFINITY : top + log2f(sum);
+}
+
+// Join the parts of each row: a warp a row, D / 32 channels a lane. Reads parts *
+// (D + 1) * 4 bytes a row.
+constexpr uint32_t kJoinWarps = 4;
+template <uint32_t D>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+k_attend_join(const AttendArgs a, const CacheView c, const PartsView parts, const uint32_t prefix_parts,
+              const uint32_t splits) {
+  constexpr uint32_t kPer = D / 32;
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint64_t id = uint64_t(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  if (id >= parts.rows) return;
+  const int32_t i = int32_t(id / a.Hq);
+  const uint32_t hq = uint32_t(id % a.Hq);
+  const RowPlace at = place_of_row(a, i);
+  if (at.seq < 0) return;
+  uint32_t n = prefix_parts;
+  if (a.has_cache) {
+    const uint32_t own = chunks_of(cache_len(a, c, at.seq), splits).parts;
+    if (own == 1 && !prefix_parts) return;  // written by the part itself
+    n += own;
   }
-  if (a.lse && lane == 0)
-    a.lse[uint64_t(i) * a.Hq + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  float top = -INFINITY;
+  for (uint32_t p = lane; p < n; p += 32) top = fmaxf(top, parts.lse[p * parts.rows + id]);
+#pragma unroll
+  for (uint32_t o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, y[kPer];
+#pragma unroll
+  for (uint32_t j = 0; j < kPer; ++j) y[j] = 0.f;
+  for (uint32_t p0 = 0; p0 < n; p0 += 32) {
+    float f = 0.f;
+    if (p0 + lane < n) {
+      const float L = parts.lse[(p0 + lane) * parts.rows + id];
+      f = L == -INFINITY ? 0.f : ex2(L - top);
+    }
+    const uint32_t here = min(32u, n - p0);
+#pragma unroll 4
+    for (uint32_t p = 0; p < here; ++p) {
+      const float w = __shfl_sync(0xffffffffu, f, p);
+      const float* src = parts.o + ((p0 + p) * parts.rows + id) * D + lane * kPer;
+      float v[4];
+      if (kPer == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x, v[1] = x.y;
+      }
+      sum += w;
+#pragma unroll
+      for (uint32_t j = 0; j < kPer; ++j) y[j] = fmaf(w, v[j], y[j]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (uint32_t j = 0; j < kPer; ++j) y[j] *= inv;
+  store_out<kPer>(a, i, hq, lane * kPer, y);
+  if (a.lse && lane == 0) a.lse[id] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// ---- how a call is divided
+
+constexpr uint32_t kSMs = 148;
+struct Division {
+  uint32_t row_tiles;      // 8-row tiles a block takes: 1 or 2
+  uint32_t row_groups;     // blocks along a sequence's query rows
+  uint32_t splits;         // parts of a sequence's cache tokens at most
+  uint32_t prefix_parts;
+  uint32_t parts;          // of a row at most
+};
+
+uint64_t parts_bytes(const AttendArgs& a, uint64_t parts) {
+  const uint64_t rows = uint64_t(a.n_rows) * a.Hq;
+  return (parts * rows * sizeof(float) + 15) / 16 * 16 + parts * rows * a.D * sizeof(float);
+}
+
+// most: parts that the workspace has room for
+Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint64_t most) {
+  Division d{1, 1, 1, a.prefix_tokens ? 1u : 0u, 1};
+  if (a.has_cache) {
+    const uint64_t rows = uint64_t(std::max(max_queries, 1u)) * a.G;
+    d.row_tiles = rows > 8 ? 2 : 1;
+    d.row_groups = uint32_t(std::min<uint64_t>((rows + 8 * d.row_tiles - 1) / (8 * d.row_tiles), 4096u));
+    // One wave of blocks (3 an SM) is filled with parts of at least 64 tokens;
+    // with more blocks than that, parts of about 1024 tokens until there are
+    // some six waves, so that sequences of different lengths even out.
+    const uint64_t wave = kSMs * 3, blocks = uint64_t(a.n_seqs) * a.H * d.row_groups;
+    const uint64_t fine = std::max<uint64_t>(1, (uint64_t(max_kv) + kLeastTiles * kTile - 1) / (kLeastTiles * kTile));
+    const uint64_t coarse = std::max<uint64_t>(1, uint64_t(max_kv) / 1024);
+    uint64_t s = std::min(fine, std::max<uint64_t>(1, wave / std::max<uint64_t>(blocks, 1)));
+    s = std::max(s, std::min(coarse, std::max<uint64_t>(1, 6 * wave / std::max<uint64_t>(blocks, 1))));
+    s = std::min<uint64_t>(s, 512);
+    if (s + d.prefix_parts > 1 && s + d.prefix_parts > most) s = most > d.prefix_parts + 1 ? most - d.prefix_parts : 1;
+    d.splits = uint32_t(s);
+  }
+  d.parts = d.prefix_parts + (a.has_cache ? d.splits : 0);
+  return d;
+}
+
+template <uint32_t FMT, uint32_t D, uint32_t R>
+cudaError_t run_cache(const AttendArgs& a, const CacheView& c, const PartsView& parts, const Division& d,
+                      cudaStream_t st) {
+  using T = CacheTile<FMT, D, R>;
+  static SmemAttr track;
+  cudaError_t e = smem_attr(track, reinterpret_cast<const void*>(k_attend_cache<FMT, D, R>), T::kSmem);
+  if (e != cudaSuccess) return e;
+  ProfRange p("attend_cache", st);
+  k_attend_cache<FMT, D, R><<<dim3(d.row_groups * d.splits, a.H, a.n_seqs), T::kThreads, T::kSmem, st>>>(
+      a, c, parts, d.prefix_parts, d.splits, d.row_groups);
+  return cudaGetLastError();
+}
+template <uint32_t FMT, uint32_t D>
+cudaError_t pick_cache(const AttendArgs& a, const CacheView& c, const PartsView& parts, const Division& d,
+                       cudaStream_t st) {
+  return d.row_tiles == 1 ? run_cache<FMT, D, 1>(a, c, parts, d, st) : run_cache<FMT, D, 2>(a, c, parts, d, st);
+}
+template <uint32_t D>
+cudaError_t run_all(const AttendArgs& a, const CacheView& c, const PartsView& parts, const Division& d,
+                    cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (a.prefix_tokens) {
+    ProfRange p("attend_prefix", st);
+    k_attend_prefix_rows<D / 32><<<dim3(a.n_rows, a.Hq), kRowWarps * 32, 0, st>>>(a, parts);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (a.has_cache) {
+    e = c.fmt == KVC_CACHE_E4M3   ? pick_cache<KVC_CACHE_E4M3, D>(a, c, parts, d, st)
+        : c.fmt == KVC_CACHE_INT8 ? pick_cache<KVC_CACHE_INT8, D>(a, c, parts, d, st)
+                                  : pick_cache<KVC_CACHE_E2M1, D>(a, c, parts, d, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (d.parts == 1 && !a.prefix_tokens) return e;
+  ProfRange p("attend_join", st);
+  const uint64_t blocks = (parts.rows + kJoinWarps - 1) / kJoinWarps;
+  k_attend_join<D><<<uint32_t(blocks), kJoinWarps * 32, 0, st>>>(a, c, parts, d.prefix_parts, d.splits);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-uint64_t attend_ws_bytes(const AttendArgs&, uint32_t, uint32_t, bool) { return 0; }
+uint64_t attend_ws_bytes(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, bool least) {
+  const Division d = divide(a, max_queries, max_kv, least ? 0 : UINT64_MAX);
+  return d.parts == 1 && !a.prefix_tokens ? 0 : parts_bytes(a, d.parts);
+}
 
-cudaError_t launch_attend(const AttendArgs& a, const CacheView& c, uint32_t, uint32_t, void*, size_t,
-                          cudaStream_t st) {
-  ProfRange p("attend_rows", st);
-  const dim3 grid(a.n_rows, a.Hq);
-  if (a.D == 64)
-    k_attend_rows<2><<<grid, kWarps * 32, 0, st>>>(a, c);
-  else
-    k_attend_rows<4><<<grid, kWarps * 32, 0, st>>>(a, c);
-  return cudaGetLastError();
+cudaError_t launch_attend(const AttendArgs& a, const CacheView& c, uint32_t max_queries, uint32_t max_kv, void* ws,
+                          size_t ws_bytes, cudaStream_t st) {
+  const uint64_t rows = uint64_t(a.n_rows) * a.Hq;
+  const uint64_t most = ws_bytes < 16 ? 0 : (ws_bytes - 16) / (rows * sizeof(float) * (a.D + 1));
+  const Division d = divide(a, max_queries, max_kv, most);
+  const uint64_t lse_bytes = (uint64_t(d.parts) * rows * sizeof(float) + 15) / 16 * 16;
+  const PartsView parts{static_cast<float*>(ws), reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + lse_bytes), rows};
+  return a.D == 64 ? run_all<64>(a, c, parts, d, st) : run_all<128>(a, c, parts, d, st);
 }
 
 }  // namespace kvc
