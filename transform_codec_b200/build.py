@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "libkvc.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cpp", "serving.cpp", "container.cu", "lossless.cu", "transform.cu", "cache.cu", "attend.cu"]
 HEADERS = ["kvc_device.cuh", "kvc_internal.h", "tcgen05.cuh", "serving.h", "cache_codes.cuh",
-           "attend_parts.cuh", "attend_cache.cuh"]
+           "attend_parts.cuh", "attend_cache.cuh", "attend_prefix.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

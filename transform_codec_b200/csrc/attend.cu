@@ -2,66 +2,10 @@
 // kvc_attend): launches, the division of work into parts, and their join.
 #include "attend_cache.cuh"
 #include "attend_parts.cuh"
+#include "attend_prefix.cuh"
 
 namespace kvc {
 namespace {
-
-// Prefix: one block per query row and head, for now.
-constexpr uint32_t kRowWarps = 4;
-__device__ inline float value16(uint32_t dtype, const void* p, int64_t at) {
-  const uint32_t w = static_cast<const uint16_t*>(p)[at];
-  return dtype == KVC_DTYPE_BF16 ? bf16_lo(w) : half2_f32(w).x;
-}
-template <uint32_t NC>
-__global__ void __launch_bounds__(kRowWarps * 32) k_attend_prefix_rows(const AttendArgs a, const PartsView parts) {
-  const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int32_t i = int32_t(blockIdx.x);
-  const uint32_t hq = blockIdx.y, h = hq / a.G;
-  const RowPlace at = place_of_row(a, i);
-  if (at.seq < 0) return;
-  float q[NC], acc[NC], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (uint32_t j = 0; j < NC; ++j) {
-    q[j] = value16(a.dtype, a.q, i * a.q_tok + hq * a.q_head + lane * NC + j) * a.scale_log2;
-    acc[j] = 0.f;
-  }
-  const int32_t n = int32_t(prefix_seen(a, at.seq));
-  for (int32_t t = int32_t(warp); t < n; t += kRowWarps) {
-    const int64_t off = h * a.p_head + int64_t(t) * a.D + lane * NC;
-    float s = 0.f;
-#pragma unroll
-    for (uint32_t j = 0; j < NC; ++j) s = fmaf(q[j], value16(a.dtype, a.pk, off + j), s);
-    for (uint32_t o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float m2 = s > m ? s : m;
-    const float f = m2 == m ? 1.f : exp2f(m - m2), p = exp2f(s - m2);
-    l = fmaf(l, f, p);
-#pragma unroll
-    for (uint32_t j = 0; j < NC; ++j) acc[j] = fmaf(acc[j], f, p * value16(a.dtype, a.pv, off + j));
-    m = m2;
-  }
-  __shared__ float sm[kRowWarps], sl[kRowWarps], so[kRowWarps][NC * 32];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (uint32_t j = 0; j < NC; ++j) so[warp][lane * NC + j] = acc[j];
-  __syncthreads();
-  if (warp) return;
-  float top = -INFINITY, sum = 0.f;
-  for (uint32_t w = 0; w < kRowWarps; ++w) top = fmaxf(top, sm[w]);
-#pragma unroll
-  for (uint32_t j = 0; j < NC; ++j) acc[j] = 0.f;
-  for (uint32_t w = 0; w < kRowWarps; ++w) {
-    const float f = sl[w] == 0.f ? 0.f : exp2f(sm[w] - top);
-    sum = fmaf(sl[w], f, sum);
-    for (uint32_t j = 0; j < NC; ++j) acc[j] = fmaf(so[w][lane * NC + j], f, acc[j]);
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const uint64_t id = uint64_t(i) * a.Hq + hq;
-  for (uint32_t j = 0; j < NC; ++j) parts.o[id * a.D + lane * NC + j] = acc[j] * inv;
-  if (lane == 0) parts.lse[id] = sum == 0.f ? -INFINITY : top + log2f(sum);
-}
 
 // Join the parts of each row: a warp a row, D / 32 channels a lane. Reads parts *
 // (D + 1) * 4 bytes a row.
@@ -101,6 +45,7 @@ k_attend_join(const AttendArgs a, const CacheView c, const PartsView parts, cons
 #pragma unroll 4
     for (uint32_t p = 0; p < here; ++p) {
       const float w = __shfl_sync(0xffffffffu, f, p);
+      if (w == 0.f) continue;  // a part that saw nothing need not have written an output
       const float* src = parts.o + ((p0 + p) * parts.rows + id) * D + lane * kPer;
       float v[4];
       if (kPer == 4) {
@@ -129,7 +74,7 @@ struct Division {
   uint32_t row_tiles;      // 8-row tiles a block takes: 1 or 2
   uint32_t row_groups;     // blocks along a sequence's query rows
   uint32_t splits;         // parts of a sequence's cache tokens at most
-  uint32_t prefix_parts;
+  uint32_t prefix_parts, prefix_blocks;  // parts of the prefix, 128-token blocks in each
   uint32_t parts;          // of a row at most
 };
 
@@ -140,7 +85,27 @@ uint64_t parts_bytes(const AttendArgs& a, uint64_t parts) {
 
 // most: parts that the workspace has room for
 Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint64_t most) {
-  Division d{1, 1, 1, a.prefix_tokens ? 1u : 0u, 1};
+  Division d{1, 1, 1, 0, 0, 1};
+  if (a.prefix_tokens) {
+    const uint64_t rows = uint64_t(a.n_rows) * a.G, room = most > uint64_t(a.has_cache) ? most - a.has_cache : 1;
+    const uint32_t nb = a.prefix_tokens / 128 + (a.prefix_tokens % 128 != 0);
+    const uint64_t units = (rows + 255) / 256 * a.H;
+    // Estimated time of n parts: waves of blocks (one an SM, 2 us to begin and
+    // end) of so many 128-token steps each (1.4 us for two tiles of rows, 0.8
+    // for one), and writing and reading back n results a row at 4 KB a ns.
+    const double step = rows <= 128 ? 0.8 : 1.4, result = double(rows) * a.H * a.D * 8.0 / 4e6;
+    double best = 0.0;
+    for (uint32_t n = 1; n <= std::min<uint64_t>({nb, room, 256}); ++n) {
+      const uint32_t per = (nb + n - 1) / n;
+      if (n > 1 && (nb + per - 1) / per != n) continue;
+      const double cost = double((units * n + kSMs - 1) / kSMs) * (2.0 + per * step) + n * result;
+      if (n == 1 || cost < best) {
+        best = cost;
+        d.prefix_parts = n;
+        d.prefix_blocks = per;
+      }
+    }
+  }
   if (a.has_cache) {
     const uint64_t rows = uint64_t(std::max(max_queries, 1u)) * a.G;
     d.row_tiles = rows > 8 ? 2 : 1;
@@ -159,6 +124,50 @@ Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint
   }
   d.parts = d.prefix_parts + (a.has_cache ? d.splits : 0);
   return d;
+}
+
+// Blocks of 128 tokens x 64 channels of a [H][T][D] 16-bit slice array.
+using EncodeMap = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeMap encode_map() {
+  static const EncodeMap fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeMap>(p);
+  }();
+  return fn;
+}
+bool slice_map(CUtensorMap& m, const AttendArgs& a, const void* base) {
+  const EncodeMap fn = encode_map();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {a.D, a.prefix_tokens, a.H};
+  // one head needs no stride; the map wants a valid one all the same
+  const cuuint64_t head = a.H > 1 ? cuuint64_t(a.p_head) * 2 : cuuint64_t(a.prefix_tokens) * a.D * 2;
+  const cuuint64_t strides[2] = {cuuint64_t(a.D) * 2, head};
+  const cuuint32_t box[3] = {64, 128, 1}, step[3] = {1, 1, 1};
+  return fn(&m, a.dtype == KVC_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <uint32_t DT, uint32_t D>
+cudaError_t run_prefix(const AttendArgs& a, const PartsView& parts, const Division& d, cudaStream_t st) {
+  using T = PrefixTile<D>;
+  static SmemAttr track;
+  cudaError_t e = smem_attr(track, reinterpret_cast<const void*>(k_attend_prefix<DT, D>), T::kSmem);
+  if (e != cudaSuccess) return e;
+  CUtensorMap k, v;
+  if (!slice_map(k, a, a.pk) || !slice_map(v, a, a.pv)) return cudaErrorInvalidValue;
+  const uint64_t tiles = (uint64_t(a.n_rows) * a.G + 255) / 256;
+  ProfRange p("attend_prefix", st);
+  k_attend_prefix<DT, D><<<dim3(uint32_t(tiles * d.prefix_parts), a.H), T::kThreads, T::kSmem, st>>>(
+      a, parts, k, v, d.prefix_parts, d.prefix_blocks, d.parts == 1);
+  return cudaGetLastError();
 }
 
 template <uint32_t FMT, uint32_t D, uint32_t R>
@@ -183,9 +192,8 @@ cudaError_t run_all(const AttendArgs& a, const CacheView& c, const PartsView& pa
                     cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.prefix_tokens) {
-    ProfRange p("attend_prefix", st);
-    k_attend_prefix_rows<D / 32><<<dim3(a.n_rows, a.Hq), kRowWarps * 32, 0, st>>>(a, parts);
-    e = cudaGetLastError();
+    e = a.dtype == KVC_DTYPE_BF16 ? run_prefix<KVC_DTYPE_BF16, D>(a, parts, d, st)
+                                  : run_prefix<KVC_DTYPE_FP16, D>(a, parts, d, st);
     if (e != cudaSuccess) return e;
   }
   if (a.has_cache) {
@@ -194,7 +202,7 @@ cudaError_t run_all(const AttendArgs& a, const CacheView& c, const PartsView& pa
                                   : pick_cache<KVC_CACHE_E2M1, D>(a, c, parts, d, st);
     if (e != cudaSuccess) return e;
   }
-  if (d.parts == 1 && !a.prefix_tokens) return e;
+  if (d.parts == 1) return e;
   ProfRange p("attend_join", st);
   const uint64_t blocks = (parts.rows + kJoinWarps - 1) / kJoinWarps;
   k_attend_join<D><<<uint32_t(blocks), kJoinWarps * 32, 0, st>>>(a, c, parts, d.prefix_parts, d.splits);
@@ -205,7 +213,7 @@ cudaError_t run_all(const AttendArgs& a, const CacheView& c, const PartsView& pa
 
 uint64_t attend_ws_bytes(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, bool least) {
   const Division d = divide(a, max_queries, max_kv, least ? 0 : UINT64_MAX);
-  return d.parts == 1 && !a.prefix_tokens ? 0 : parts_bytes(a, d.parts);
+  return d.parts == 1 ? 0 : parts_bytes(a, d.parts);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, const CacheView& c, uint32_t max_queries, uint32_t max_kv, void* ws,

@@ -100,7 +100,11 @@ int attend_args(const kvc_attend_desc* d, AttendArgs& a, CacheView& cv, bool poi
   a.o_tok = d->out_token_stride;
   a.o_head = d->out_head_stride;
   a.p_head = d->prefix_head_stride;
-  a.scale_log2 = float(double(d->scale) * 1.4426950408889634);
+  // a scale of (almost) zero weighs all tokens alike; kept off zero, where a
+  // hidden token's -infinity would lose its meaning
+  const double sl = double(d->scale) * 1.4426950408889634;
+  a.scale_log2 = std::fabs(sl) < 1e-30 ? 1e-30f : float(sl);
+  if (!std::isfinite(a.scale_log2)) return KVC_ERR_INVALID;
   a.dtype = d->dtype;
   a.n_rows = d->n_rows;
   a.Hq = d->n_q_heads;
