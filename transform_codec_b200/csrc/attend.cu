@@ -219,7 +219,8 @@ uint64_t attend_ws_bytes(const AttendArgs& a, uint32_t max_queries, uint32_t max
 cudaError_t launch_attend(const AttendArgs& a, const CacheView& c, uint32_t max_queries, uint32_t max_kv, void* ws,
                           size_t ws_bytes, cudaStream_t st) {
   const uint64_t rows = uint64_t(a.n_rows) * a.Hq;
-  const uint64_t most = ws_bytes < 16 ? 0 : (ws_bytes - 16) / (rows * sizeof(float) * (a.D + 1));
+  uint64_t most = ws_bytes / (rows * sizeof(float) * (a.D + 1));
+  if (most && parts_bytes(a, most) > ws_bytes) --most;  // the results begin at a multiple of 16 bytes
   const Division d = divide(a, max_queries, max_kv, most);
   const uint64_t lse_bytes = (uint64_t(d.parts) * rows * sizeof(float) + 15) / 16 * 16;
   const PartsView parts{static_cast<float*>(ws), reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + lse_bytes), rows};

@@ -6,12 +6,14 @@
 // D operations against 512 D bytes, beyond the card's operations per byte; with
 // few rows it is the reading that bounds.
 //
-// A block of 10 warps: two groups of four do the softmax of one 128-row tile
-// each, one row a thread; one warp brings K and V blocks by TMA (128-byte
-// swizzle) through a ring; one issues the products. Two tiles take turns, so the
+// A block of 12 warps: two groups of four do the softmax of one 128-row tile
+// each, one row a thread; the third group's warps bring K blocks, bring V blocks
+// (TMA, 128-byte swizzle, a ring each), issue Q K^T and issue P V, and leave
+// registers to the others: 200 * 256 + 104 * 128 is the 168 * 384 that the block
+// starts with. Two tiles take turns, so the
 // products of one run while the other's softmax does:
 //     S_r = Q_r K_j^T                        (Q, K in shared memory, S in tensor memory)
-//     P_r = 2^(scale S_r - m_r), 16 bits     (threads; P over S in tensor memory)
+//     P_r = 2^(scale S_r - m_r), 16 bits     (threads; back to tensor memory)
 //     O_r += P_r V_j                         (P in tensor memory, V token-major in shared memory)
 // With more than 128 rows the tiles are 256 different rows on the same blocks;
 // with fewer they are the same rows on alternate blocks, joined at the end.
@@ -37,6 +39,30 @@ namespace {
 
 constexpr uint32_t kDrainPolls = 1u << 22;  // waits for what is in flight, in every build
 
+// A bounded wait that another role's stop ends too.
+__device__ inline bool wait_or_stop(uint32_t bar, uint32_t parity, const volatile uint32_t* stop) {
+  for (uint32_t i = 0; i + 1 <= KVC_MMA_WAIT_POLLS; ++i) {
+    uint32_t there;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(there)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (there) return true;
+    if (*stop) return false;
+  }
+  return false;
+}
+__device__ inline bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ inline void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ inline void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_addr(bar)) : "memory");
 }
@@ -95,28 +121,59 @@ __device__ inline void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
+// The loads' end: values in v are used after it, not before.
+__device__ inline void tmem_landed32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
+// pairs of fp32 at once
+__device__ inline float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ inline float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ inline float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
 __device__ inline void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 template <uint32_t D>
 struct PrefixTile {
-  static constexpr uint32_t kThreads = 320, kRows = 128, kTokens = 128;
+  static constexpr uint32_t kThreads = 384, kRows = 128, kTokens = 128;
   static constexpr uint32_t kBlock = kTokens * D * 2;  // bytes of a K or V block, or of a Q tile
   static constexpr uint32_t kHalf = kTokens * 128;     // 64 channels of it
-  static constexpr uint32_t kStages = D == 128 ? 5 : 8;
-  static constexpr uint32_t kRing = 2 * kBlock;        // offset: after two Q tiles
-  static constexpr uint32_t kBars = kRing + kStages * kBlock;
+  static constexpr uint32_t kKStages = D == 128 ? 2 : 4, kVStages = D == 128 ? 3 : 4;
+  static constexpr uint32_t kK = 2 * kBlock, kV = kK + kKStages * kBlock;  // rings, after two Q tiles
+  static constexpr uint32_t kBars = kV + kVStages * kBlock;
   static constexpr uint32_t kSmem = 1024 + kBars + 256;
-  static constexpr uint32_t kO = 256;                  // tensor-memory column of O_0; S_r at 128 r
+  static constexpr uint32_t kP = 128, kO = 256;        // tensor-memory columns of P_0 and O_0; S at 0
 };
 struct PrefixBars {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], pv_done[2], drain;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], s_free, p_full[2], o_done[2], drain[2], tail;
   uint32_t tmem, stop, seen;
 };
 static_assert(sizeof(PrefixBars) <= 256, "barrier area");
 
 // grid (prefix parts * row blocks, H)
 template <uint32_t DT, uint32_t D>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
 k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const uint32_t n_parts, const uint32_t blocks_per_part,
                 const uint32_t direct) {
@@ -125,23 +182,28 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   PrefixBars& B = *reinterpret_cast<PrefixBars*>(smem + T::kBars);
-  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31u;
+  const uint32_t tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31u;
   const uint32_t part = blockIdx.x % n_parts, h = blockIdx.y;
   const uint64_t total_rows = uint64_t(a.n_rows) * a.G;
   const bool same_rows = total_rows <= T::kRows;  // both tiles hold the same rows
   const uint64_t row0 = uint64_t(blockIdx.x / n_parts) * (2 * T::kRows);
 
   if (tid == 0) {
-    for (uint32_t i = 0; i < T::kStages; ++i) {
-      tc::mbar_init(&B.full[i], 1);
-      tc::mbar_init(&B.empty[i], 1);
+    for (uint32_t i = 0; i < 4; ++i) {
+      tc::mbar_init(&B.k_full[i], 1);
+      tc::mbar_init(&B.k_empty[i], 1);
+      tc::mbar_init(&B.v_full[i], 1);
+      tc::mbar_init(&B.v_empty[i], 1);
     }
     for (uint32_t r = 0; r < 2; ++r) {
       tc::mbar_init(&B.s_full[r], 1);
       tc::mbar_init(&B.p_full[r], T::kRows);
-      tc::mbar_init(&B.pv_done[r], 1);
+      tc::mbar_init(&B.o_done[r], 1);
     }
-    tc::mbar_init(&B.drain, 1);
+    tc::mbar_init(&B.s_free, T::kRows);
+    tc::mbar_init(&B.drain[0], 1);
+    tc::mbar_init(&B.drain[1], 1);
+    tc::mbar_init(&B.tail, 32);
     B.stop = 0;
     B.seen = 0;
   }
@@ -166,17 +228,24 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
     }
     if (see <= token0) see = 0;
     if (see) atomicMax(&B.seen, see);
-    const uint16_t* src =
-        static_cast<const uint16_t*>(a.q) + int64_t(row / a.G) * a.q_tok + int64_t(h * a.G + row % a.G) * a.q_head;
+    // rows with something to see; a warp brings its 32 rows, whole rows at a time
+    const int64_t src = int64_t(row / a.G) * a.q_tok + int64_t(h * a.G + uint32_t(row % a.G)) * a.q_head;
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale goes into q's signs
+    constexpr uint32_t kLanes = D / 8, kAtOnce = 32 / kLanes;
+    uint4 w[32 / kAtOnce];
 #pragma unroll
-    for (uint32_t i = 0; i < D / 8; ++i) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (see) {
-        w = *reinterpret_cast<const uint4*>(src + i * 8);
-        w.x ^= flip, w.y ^= flip, w.z ^= flip, w.w ^= flip;
-      }
-      *reinterpret_cast<uint4*>(smem + r * T::kBlock + tc::sw128_offset(my, i * 16, T::kRows)) = w;
+    for (uint32_t i = 0; i < 32 / kAtOnce; ++i) {
+      const uint32_t from = i * kAtOnce + lane / kLanes;
+      const int64_t at = __shfl_sync(0xffffffffu, src, from);
+      const bool used = __shfl_sync(0xffffffffu, see, from) != 0;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (used) w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + lane % kLanes * 8));
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < 32 / kAtOnce; ++i) {
+      const uint32_t to = (warp & 3u) * 32 + i * kAtOnce + lane / kLanes;
+      *reinterpret_cast<uint4*>(smem + r * T::kBlock + tc::sw128_offset(to, lane % kLanes * 16, T::kRows)) =
+          make_uint4(w[i].x ^ flip, w[i].y ^ flip, w[i].z ^ flip, w[i].w ^ flip);
     }
     tc::fence_async_smem();
   }
@@ -186,125 +255,138 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
   const uint32_t seen = B.seen;  // the longest share in this block's rows
   const uint32_t nb = seen > token0 ? (seen - token0 + T::kTokens - 1) / T::kTokens : 0u;
   const uint32_t tmem = B.tmem;
-  // items: (tile, token block) pairs in the order of their products
-  const uint32_t items = same_rows ? nb : 2 * nb;
-  // K and V blocks enter the ring in the order they are used
-  auto k_at = [&](uint32_t b) { return same_rows ? (b ? 2 * b - 1 : 0u) : 2 * b; };
-  auto v_at = [&](uint32_t b) { return same_rows && b + 1 < nb ? 2 * b + 2 : 2 * b + 1; };
   volatile uint32_t* stop = &B.stop;
-  // one answer for the whole warp
+  // one answer for the whole warp; another role's stop ends the wait too
   auto await = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, !*stop && tc::mbar_wait(bar, parity, KVC_MMA_WAIT_POLLS)) != 0;
+    return __all_sync(0xffffffffu, wait_or_stop(tc::smem_addr(bar), parity, stop)) != 0;
   };
 
-  if (warp == 8) {
-    // ---- loads
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if (warp == 8 || warp == 11) {
+    // ---- loads: K blocks, V blocks
+    const bool is_v = warp == 11;
+    const uint32_t stages = is_v ? T::kVStages : T::kKStages;
+    uint64_t* full = is_v ? B.v_full : B.k_full;
+    uint64_t* empty = is_v ? B.v_empty : B.k_empty;
+    uint8_t* ring = smem + (is_v ? T::kV : T::kK);
+    uint32_t b = 0;
     if (lane == 0) {
-      uint32_t issued = 0;
-      for (; issued < 2 * nb && !*stop; ++issued) {
-        const uint32_t s = issued % T::kStages, use = issued / T::kStages;
-        if (use && !tc::mbar_wait(&B.empty[s], (use - 1) & 1u, KVC_MMA_WAIT_POLLS)) {
+      const CUtensorMap* map = is_v ? &vmap : &kmap;
+      for (; b < nb; ++b) {
+        const uint32_t s = b % stages, use = b / stages;
+        if (use && !wait_or_stop(tc::smem_addr(&empty[s]), (use - 1) & 1u, stop)) {
           *stop = 1;
           break;
         }
-        // which block is this?
-        bool is_v;
-        uint32_t b;
-        if (!same_rows) {
-          is_v = issued & 1u;
-          b = issued >> 1;
-        } else if (issued == 0) {
-          is_v = false;
-          b = 0;
-        } else if (issued == 2 * nb - 1) {
-          is_v = true;
-          b = nb - 1;
-        } else {
-          is_v = !(issued & 1u);
-          b = is_v ? (issued - 2) / 2 : (issued + 1) / 2;
-        }
-        const CUtensorMap* map = is_v ? &vmap : &kmap;
-        const uint32_t dst = tc::smem_addr(smem + T::kRing + s * T::kBlock);
-        mbar_expect(&B.full[s], T::kBlock);
+        const uint32_t dst = tc::smem_addr(ring + s * T::kBlock);
+        mbar_expect(&full[s], T::kBlock);
 #pragma unroll
         for (uint32_t x = 0; x < D / 64; ++x)
-          tma_load3(dst + x * T::kHalf, map, int32_t(x * 64), int32_t(token0 + b * T::kTokens), int32_t(h), &B.full[s]);
+          tma_load3(dst + x * T::kHalf, map, int32_t(x * 64), int32_t(token0 + b * T::kTokens), int32_t(h), &full[s]);
       }
       // what was issued lands before the block leaves, also after a stop
-      for (uint32_t i = issued > T::kStages ? issued - T::kStages : 0; i < issued; ++i)
-        tc::mbar_wait(&B.full[i % T::kStages], (i / T::kStages) & 1u, kDrainPolls);
+      for (uint32_t i = b > stages ? b - stages : 0; i < b; ++i)
+        tc::mbar_wait(&full[i % stages], (i / stages) & 1u, kDrainPolls);
     }
-  } else if (warp == 9) {
-    // ---- products
-    const uint32_t s_desc = idesc_16(kBf16, 128, 128, false), o_desc = idesc_16(kBf16, 128, D, true);
+    b = __shfl_sync(0xffffffffu, b, 0);
+    const uint32_t first = (seen - token0) % T::kTokens;
+    if (is_v && b == nb && nb && first) {
+      // tokens of the last block that no row of this block sees may hold anything;
+      // their weights are zero, and so must be what they multiply
+      const uint32_t n = (T::kTokens - first) * 8;
+      uint8_t* v = ring + (nb - 1) % stages * T::kBlock;
+      for (uint32_t i = lane; i < n * (D / 64); i += 32)
+        *reinterpret_cast<uint4*>(v + (i / n) * T::kHalf + first * 128 + (i % n) * 16) = make_uint4(0, 0, 0, 0);
+      tc::fence_async_smem();
+      mbar_arrive(&B.tail);
+    }
+  } else if (nb) {
+    // ---- products: one warp issues Q K^T, the other P V. The issue of a product
+    // waits for the tensor pipe, a few products deep, and a wait for a barrier that
+    // is already there still takes some 200 clocks: with one warp for both the
+    // pipe ran dry in between. One lane issues, the whole warp walks along, so that
+    // operands are uniform.
     bool ok = true;
-    auto await_full = [&](uint32_t at) {
-      ok = await(&B.full[at % T::kStages], (at / T::kStages) & 1u);
+    uint32_t stage = 0, phase = 0;  // of the warp's next block
+    auto await_u = [&](uint32_t bar, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop)) != 0;
+      return ok;
     };
-    auto issue_s = [&](uint32_t it) {
-      const uint32_t t = it & 1u, b = same_rows ? it : it >> 1, at = k_at(b);
-      if (same_rows || !t) await_full(at);
-      if (!ok) return;
-      tc::fence_after_sync();
-      if (lane == 0) {
-        const uint32_t q = tc::smem_addr(smem + t * T::kBlock), k = tc::smem_addr(smem + T::kRing + (at % T::kStages) * T::kBlock);
-#pragma unroll
-        for (uint32_t s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s / 4) * T::kHalf + (s % 4) * 32;
-          const uint64_t qd = tc::desc_sw128(q + off), kd = tc::desc_sw128(k + off);
-          tc::mma_bf16(tmem + t * 128, qd, kd, s_desc, s != 0);
-        }
-        tc::mma_commit(&B.s_full[t]);
-        if (same_rows || t) tc::mma_commit(&B.empty[at % T::kStages]);
-      }
-      __syncwarp();
-    };
-    if (items > 0) issue_s(0);
-    if (items > 1) issue_s(1);
-    for (uint32_t it = 0; it < items && ok; ++it) {
-      const uint32_t t = it & 1u, b = same_rows ? it : it >> 1, at = v_at(b), turn = it >> 1;
-      if (same_rows || !t) {
-        await_full(at);
+    if (warp == 9) {
+      const uint32_t s_desc = idesc_16(kBf16, 128, 128, false);
+      const uint64_t q0 = tc::desc_sw128(tc::smem_addr(smem)), k0 = tc::desc_sw128(tc::smem_addr(smem + T::kK));
+      const uint32_t full0 = tc::smem_addr(&B.k_full[0]), empty0 = tc::smem_addr(&B.k_empty[0]),
+                     s_full0 = tc::smem_addr(&B.s_full[0]), s_free = tc::smem_addr(&B.s_free);
+      // One S at a time stands in tensor memory: the next may come once the last has
+      // been taken to registers. So the S of a tile is there when its softmax
+      // returns from the one before.
+      const uint32_t items = same_rows ? nb : 2 * nb;
+      for (uint32_t it = 0; it < items; ++it) {
+        const uint32_t t = it & 1u;
+        const bool takes = same_rows || !t, frees = same_rows || t;
+        if (takes) await_u(full0 + stage * 8, phase);
+        if (it) await_u(s_free, (it - 1) & 1u);
         if (!ok) break;
-        // tokens that no row of the block sees may hold anything: their weights are
-        // zero, and so must be what they are multiplied with
-        const uint32_t base = token0 + b * T::kTokens;
-        if (base + T::kTokens > seen) {
-          uint8_t* v = smem + T::kRing + (at % T::kStages) * T::kBlock;
-          const uint32_t first = seen - base, n = (T::kTokens - first) * 8;
-          for (uint32_t i = lane; i < n * (D / 64); i += 32)
-            *reinterpret_cast<uint4*>(v + (i / n) * T::kHalf + first * 128 + (i % n) * 16) = make_uint4(0, 0, 0, 0);
-          tc::fence_async_smem();
-          __syncwarp();
+        tc::fence_after_sync();
+        const uint64_t q = q0 + t * (T::kBlock >> 4), k = k0 + stage * (T::kBlock >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (uint32_t s = 0; s < D / 16; ++s) {
+            const uint32_t off = ((s / 4) * T::kHalf + (s % 4) * 32) >> 4;
+            tc::mma_bf16(tmem, q + off, k + off, s_desc, s != 0);
+          }
+          commit(s_full0 + t * 8);
+          if (frees) commit(empty0 + stage * 8);
+        }
+        if (frees && ++stage == T::kKStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      ok = await(&B.p_full[t], turn & 1u);
-      if (!ok) break;
-      tc::fence_after_sync();
-      if (lane == 0) {
-        const uint32_t v = tc::smem_addr(smem + T::kRing + (at % T::kStages) * T::kBlock);
+    } else {
+      const uint32_t o_desc = idesc_16(kBf16, 128, D, true);
+      const uint64_t v0 = desc_mn_sw128(tc::smem_addr(smem + T::kV), T::kHalf);
+      const uint32_t full0 = tc::smem_addr(&B.v_full[0]), empty0 = tc::smem_addr(&B.v_empty[0]),
+                     p_full0 = tc::smem_addr(&B.p_full[0]), o_done0 = tc::smem_addr(&B.o_done[0]);
+      const bool tail = (seen - token0) % T::kTokens != 0;
+      const uint32_t items = same_rows ? nb : 2 * nb;
+      for (uint32_t it = 0; it < items; ++it) {
+        const uint32_t t = it & 1u, turn = it >> 1;
+        const bool takes = same_rows || !t, frees = same_rows || t;
+        if (takes) {
+          await_u(full0 + stage * 8, phase);
+          if (tail && (same_rows ? it : turn) + 1 == nb) await_u(tc::smem_addr(&B.tail), 0);
+        }
+        await_u(p_full0 + t * 8, turn & 1u);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t v = v0 + stage * (T::kBlock >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t s = 0; s < T::kTokens / 16; ++s)
-          mma_ts(tmem + T::kO + t * D, tmem + t * 128 + s * 8, desc_mn_sw128(v + s * 2048, T::kHalf), o_desc,
-                 turn != 0 || s != 0);
-        tc::mma_commit(&B.pv_done[t]);
-        if (same_rows || t) tc::mma_commit(&B.empty[at % T::kStages]);
+          for (uint32_t s = 0; s < T::kTokens / 16; ++s)
+            mma_ts(tmem + T::kO + t * D, tmem + T::kP + t * 64 + s * 8, v + s * (2048 >> 4), o_desc, turn != 0 || s != 0);
+          commit(o_done0 + t * 8);
+          if (frees) commit(empty0 + stage * 8);
+        }
+        if (frees && ++stage == T::kVStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      __syncwarp();
-      // S over P of the same tile: products run in the order of their issue
-      if (it + 2 < items) issue_s(it + 2);
     }
     if (!ok) *stop = 1;
-    if (lane == 0) {  // products in flight end before tensor memory is given back, also after a stop
-      tc::mma_commit(&B.drain);
-      tc::mbar_wait(&B.drain, 0, kDrainPolls);
-    }
+    // all products have ended before tensor memory is given back, also after a stop
+    if (elect_one()) commit(tc::smem_addr(&B.drain[warp - 9]));
+    tc::mbar_wait(&B.drain[warp - 9], 0, kDrainPolls);
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax of row `my` of tile r
     const uint32_t turns = same_rows ? (nb + 1 - r) / 2 : nb;
     const uint32_t lanes = ((warp & 3u) * 32u) << 16;  // this warp's lanes of tensor memory
-    const uint32_t s_at = tmem + lanes + r * 128, o_at = tmem + lanes + T::kO + r * D;
+    const uint32_t s_at = tmem + lanes, p_at = s_at + T::kP + r * 64, o_at = s_at + T::kO + r * D;
     const float scale = fabsf(a.scale_log2);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -313,63 +395,87 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       ok = await(&B.s_full[r], n & 1u);
       if (!ok) break;
       tc::fence_after_sync();
-      float s[128];
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) tmem_ld32(s_at + 32 * i, s + 32 * i);
-      tc::tmem_wait_ld();
       const uint32_t base = token0 + b * T::kTokens;
       const uint32_t left = see > base ? see - base : 0u;  // tokens of the block that the row sees
-      if (__any_sync(0xffffffffu, left < T::kTokens)) {
+      const bool none = left == 0, part_seen = left < T::kTokens && !none;
+      const bool border = __any_sync(0xffffffffu, part_seen), skips = __any_sync(0xffffffffu, none);
+      float x[128];
 #pragma unroll
-        for (uint32_t i = 0; i < 128; ++i) s[i] = i < left ? s[i] : -INFINITY;
+      for (uint32_t c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x + 32 * c);
+#pragma unroll
+      for (uint32_t c = 0; c < 4; ++c) tmem_landed32(x + 32 * c);
+      tc::fence_before_sync();
+      mbar_arrive(&B.s_free);
+      if (border) {
+#pragma unroll
+        for (uint32_t i = 0; i < 128; ++i) x[i] = i < left ? x[i] : -INFINITY;
       }
-      float top = s[0];
+      float top[4];
 #pragma unroll
-      for (uint32_t i = 1; i < 128; ++i) top = fmaxf(top, s[i]);
-      top *= scale;
-      const bool move = top > m + 15.f;
-      if (__any_sync(0xffffffffu, move)) {
-        const float to = move ? top - 7.f : m;
-        const float f = move ? exp2f(m - to) : 1.f;
-        m = to;
+      for (uint32_t i = 0; i < 4; ++i) top[i] = max3(x[i], x[4 + i], x[8 + i]);
+#pragma unroll
+      for (uint32_t i = 12; i < 124; i += 8)
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) top[j] = max3(top[j], x[i + j], x[i + 4 + j]);
+      // (x[124 .. 127] are left)
+#pragma unroll
+      for (uint32_t j = 0; j < 4; ++j) top[j] = max3(top[j], x[124 + j], x[124 + j]);
+      float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]) * scale;
+      const bool odd = !(high < INFINITY);  // a NaN or an infinity among the scores
+      if (none) high = -INFINITY;
+      const bool move = high > m + 15.f;
+      const bool moves = __any_sync(0xffffffffu, move);
+      float f = 1.f;
+      if (moves && move) {
+        f = exp2f(m - (high - 7.f));
+        m = high - 7.f;
         l *= f;
-        if (n) {
-          ok = await(&B.pv_done[r], (n - 1) & 1u);
-          if (!ok) break;
-          tc::fence_after_sync();
+      }
+      // a row that has seen nothing yet: its weights are zero
+      const float ref = m == -INFINITY ? 0.f : -m;
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t p[64];
+#pragma unroll
+      for (uint32_t i = 0; i < 64; ++i) {
+        float2 e = fma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale), make_float2(ref, ref));
+        e.x = ex2(e.x);
+        e.y = ex2(e.y);
+        sum[i & 1] = add2(sum[i & 1], e);
+        p[i] = pack16<DT>(e.x, e.y);
+      }
+      sum[0] = add2(sum[0], sum[1]);
+      float add = sum[0].x + sum[0].y;
+      if (odd) add = __uint_as_float(0x7fc00000u);
+      if (skips) {
+        const uint32_t keep = none ? 0u : 0xffffffffu;
+#pragma unroll
+        for (uint32_t i = 0; i < 64; ++i) p[i] &= keep;
+        if (none) add = 0.f;
+      }
+      l += add;
+      if (n) {  // the product of the last P has read it, and O is complete
+        ok = await(&B.o_done[r], (n - 1) & 1u);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (moves) {
 #pragma unroll
           for (uint32_t i = 0; i < D / 32; ++i) {
             float o[32];
             tmem_ld32(o_at + 32 * i, o);
-            tc::tmem_wait_ld();
+            tmem_landed32(o);
 #pragma unroll
             for (uint32_t j = 0; j < 32; ++j) o[j] *= f;
             tmem_st32(o_at + 32 * i, reinterpret_cast<const uint32_t*>(o));
           }
-          tmem_wait_st();
         }
       }
-      // a row that has seen nothing yet: every weight is zero
-      const float ref = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) {
-        uint32_t p[32];
-#pragma unroll
-        for (uint32_t j = 0; j < 32; ++j) {
-          const float x = ex2(fmaf(s[64 * i + 2 * j], scale, -ref)), y = ex2(fmaf(s[64 * i + 2 * j + 1], scale, -ref));
-          sum[j & 1] += x;
-          sum[2 + (j & 1)] += y;
-          p[j] = pack16<DT>(x, y);
-        }
-        tmem_st32(s_at + 32 * i, p);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st32(p_at, p);
+      tmem_st32(p_at + 32, p + 32);
       tmem_wait_st();
       tc::fence_before_sync();
       mbar_arrive(&B.p_full[r]);
     }
-    if (ok && turns) ok = await(&B.pv_done[r], (turns - 1) & 1u);  // the tile's last products
+    if (ok && turns) ok = await(&B.o_done[r], (turns - 1) & 1u);  // the last products
     if (!ok) {
       *stop = 1;
       if (a.res) *reinterpret_cast<volatile int32_t*>(&a.res->status) = KVC_ERR_TIMEOUT;
@@ -377,7 +483,7 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
     tc::fence_after_sync();
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float L = l == 0.f ? -INFINITY : m + log2f(l);
-    float* other = reinterpret_cast<float*>(smem + T::kRing);  // the second tile's results: [D][128], then L
+    float* other = reinterpret_cast<float*>(smem + T::kK);  // the second tile's results: [D][128], then L
     float f0 = inv, f1 = 0.f, LL = L;
     if (same_rows) {
       // every load and product of this block has ended once both groups are here
@@ -385,9 +491,9 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       if (r == 1) {
 #pragma unroll
         for (uint32_t i = 0; i < D / 32; ++i) {
-          float o[32];
+          float o[32] = {};
           if (turns) tmem_ld32(o_at + 32 * i, o);
-          tc::tmem_wait_ld();
+          tmem_landed32(o);
 #pragma unroll
           for (uint32_t j = 0; j < 32; ++j) other[(32 * i + j) * 128 + my] = turns && l != 0.f ? o[j] * inv : 0.f;
         }
@@ -405,27 +511,44 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       }
     }
     if (r == 0 || !same_rows) {
+      // 32 channels of the warp's 32 rows at a time go through the tile's Q space,
+      // so that rows leave 128 bytes at a time
       const int32_t i0 = int32_t(row / a.G);
       const uint32_t hq = h * a.G + uint32_t(row % a.G);
       const uint64_t id = uint64_t(i0) * a.Hq + hq;
       const uint64_t at = uint64_t(part) * parts.rows + id;
+      float4* stage = reinterpret_cast<float4*>(smem + r * T::kBlock + (warp & 3u) * 4096);
+      const bool writes = live && (direct || LL != -INFINITY);
 #pragma unroll
       for (uint32_t i = 0; i < D / 32; ++i) {
-        float o[32];
+        float o[32] = {};
         if (turns) tmem_ld32(o_at + 32 * i, o);
-        tc::tmem_wait_ld();
+        tmem_landed32(o);
 #pragma unroll
         for (uint32_t j = 0; j < 32; ++j) {
           o[j] = turns && l != 0.f ? o[j] * f0 : 0.f;
           if (same_rows) o[j] = fmaf(other[(32 * i + j) * 128 + my], f1, o[j]);
         }
-        if (live && direct) {
-          store_out<32>(a, i0, hq, 32 * i, o);
-        } else if (live && !direct && LL != -INFINITY) {
-          float4* dst = reinterpret_cast<float4*>(parts.o + at * D + 32 * i);
 #pragma unroll
-          for (uint32_t j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        for (uint32_t j = 0; j < 8; ++j)
+          stage[lane * 8 + (j ^ (lane & 7u))] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        __syncwarp();
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+          const uint32_t rr = k * 4 + lane / 8, u = lane & 7u;
+          const float4 v = stage[rr * 8 + (u ^ (rr & 7u))];
+          const bool w = __shfl_sync(0xffffffffu, writes, rr);
+          const uint64_t to = __shfl_sync(0xffffffffu, at, rr);
+          const int32_t ti = __shfl_sync(0xffffffffu, i0, rr);
+          const uint32_t th = __shfl_sync(0xffffffffu, hq, rr);
+          if (w && direct) {
+            const float y[4] = {v.x, v.y, v.z, v.w};
+            store_out<4>(a, ti, th, 32 * i + 4 * u, y);
+          } else if (w) {
+            *reinterpret_cast<float4*>(parts.o + to * D + 32 * i + 4 * u) = v;
+          }
         }
+        __syncwarp();
       }
       if (live) {
         if (!direct)
