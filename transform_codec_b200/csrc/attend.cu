@@ -7,66 +7,6 @@
 namespace kvc {
 namespace {
 
-// Join the parts of each row: a warp a row, D / 32 channels a lane. Reads parts *
-// (D + 1) * 4 bytes a row.
-constexpr uint32_t kJoinWarps = 4;
-template <uint32_t D>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-k_attend_join(const AttendArgs a, const CacheView c, const PartsView parts, const uint32_t prefix_parts,
-              const uint32_t splits) {
-  constexpr uint32_t kPer = D / 32;
-  const uint32_t lane = threadIdx.x & 31u;
-  const uint64_t id = uint64_t(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (id >= parts.rows) return;
-  const int32_t i = int32_t(id / a.Hq);
-  const uint32_t hq = uint32_t(id % a.Hq);
-  const RowPlace at = place_of_row(a, i);
-  if (at.seq < 0) return;
-  uint32_t n = prefix_parts;
-  if (a.has_cache) {
-    const uint32_t own = chunks_of(cache_len(a, c, at.seq), splits).parts;
-    if (own == 1 && !prefix_parts) return;  // written by the part itself
-    n += own;
-  }
-  float top = -INFINITY;
-  for (uint32_t p = lane; p < n; p += 32) top = fmaxf(top, parts.lse[p * parts.rows + id]);
-#pragma unroll
-  for (uint32_t o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float sum = 0.f, y[kPer];
-#pragma unroll
-  for (uint32_t j = 0; j < kPer; ++j) y[j] = 0.f;
-  for (uint32_t p0 = 0; p0 < n; p0 += 32) {
-    float f = 0.f;
-    if (p0 + lane < n) {
-      const float L = parts.lse[(p0 + lane) * parts.rows + id];
-      f = L == -INFINITY ? 0.f : ex2(L - top);
-    }
-    const uint32_t here = min(32u, n - p0);
-#pragma unroll 4
-    for (uint32_t p = 0; p < here; ++p) {
-      const float w = __shfl_sync(0xffffffffu, f, p);
-      if (w == 0.f) continue;  // a part that saw nothing need not have written an output
-      const float* src = parts.o + ((p0 + p) * parts.rows + id) * D + lane * kPer;
-      float v[4];
-      if (kPer == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        v[0] = x.x, v[1] = x.y;
-      }
-      sum += w;
-#pragma unroll
-      for (uint32_t j = 0; j < kPer; ++j) y[j] = fmaf(w, v[j], y[j]);
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (uint32_t j = 0; j < kPer; ++j) y[j] *= inv;
-  store_out<kPer>(a, i, hq, lane * kPer, y);
-  if (a.lse && lane == 0) a.lse[id] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-}
-
 // ---- how a call is divided
 
 constexpr uint32_t kSMs = 148;
@@ -77,6 +17,108 @@ struct Division {
   uint32_t prefix_parts, prefix_blocks;  // parts of the prefix, 128-token blocks in each
   uint32_t parts;          // of a row at most
 };
+
+// Join the parts of each row, D / 32 channels a lane; reads parts * (D + 1) * 4
+// bytes a row. A warp takes a row, or kWarps warps its parts in turn where there
+// are many: with 64 rows of 55 parts (one query, 131,072 tokens) one warp a row
+// spent 59 us on loads one after another, eight spend 5.
+constexpr uint32_t kJoinThreads = 256;
+template <uint32_t D, uint32_t kWarps>
+__global__ void __launch_bounds__(kJoinThreads)
+k_attend_join(const AttendArgs a, const CacheView c, const PartsView parts, const uint32_t prefix_parts,
+              const uint32_t splits) {
+  constexpr uint32_t kPer = D / 32, kRows = kJoinThreads / 32 / kWarps;
+  __shared__ float ssum[kRows][kWarps], sy[kWarps > 1 ? kRows * kWarps : 1][D];
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, part0 = warp % kWarps;
+  const uint64_t id = uint64_t(blockIdx.x) * kRows + warp / kWarps;
+  int32_t i = 0;
+  uint32_t hq = 0, n = 0;
+  if (id < parts.rows) {
+    i = int32_t(id / a.Hq);
+    hq = uint32_t(id % a.Hq);
+    const RowPlace at = place_of_row(a, i);
+    if (at.seq >= 0) {
+      n = prefix_parts;
+      if (a.has_cache) {
+        const uint32_t own = chunks_of(cache_len(a, c, at.seq), splits).parts;
+        n = own == 1 && !prefix_parts ? 0u : n + own;  // one part alone has written the row itself
+      }
+    }
+  }
+  const float* lse = parts.lse + id;
+  float top = -INFINITY;
+  for (uint32_t p = lane; p < n; p += 32) top = fmaxf(top, lse[p * parts.rows]);
+#pragma unroll
+  for (uint32_t o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float sum = 0.f, y[kPer];
+#pragma unroll
+  for (uint32_t j = 0; j < kPer; ++j) y[j] = 0.f;
+  // this warp's parts: part0, part0 + kWarps, ..; 32 weights at a time, one a lane
+  for (uint32_t p0 = part0; p0 < n; p0 += 32 * kWarps) {
+    float f = 0.f;
+    const uint32_t mine = p0 + lane * kWarps;
+    if (mine < n) {
+      const float L = lse[mine * parts.rows];
+      f = L == -INFINITY ? 0.f : ex2(L - top);
+    }
+    const uint32_t here = min(32u, (n - p0 + kWarps - 1) / kWarps);
+    for (uint32_t q = 0; q < here; q += 4) {
+      float w[4], v[4][kPer];
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u) {
+        w[u] = __shfl_sync(0xffffffffu, f, (q + u) & 31u);
+        if (q + u >= here) w[u] = 0.f;
+        // a part that saw nothing need not have written an output
+        const float* src = parts.o + ((p0 + (q + u) * kWarps) * parts.rows + id) * D + lane * kPer;
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) v[u][j] = 0.f;
+        if (w[u] != 0.f) {
+          if constexpr (kPer == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[u][0] = x.x, v[u][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (uint32_t u = 0; u < 4; ++u) {
+        sum += w[u];
+#pragma unroll
+        for (uint32_t j = 0; j < kPer; ++j) y[j] = fmaf(w[u], v[u][j], y[j]);
+      }
+    }
+  }
+  if (kWarps > 1) {
+    if (lane == 0) ssum[warp / kWarps][part0] = sum;
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) sy[warp][lane * kPer + j] = y[j];
+    __syncthreads();
+    if (part0) return;
+    for (uint32_t w = 1; w < kWarps; ++w) {
+      sum += ssum[warp / kWarps][w];
+#pragma unroll
+      for (uint32_t j = 0; j < kPer; ++j) y[j] += sy[warp + w][lane * kPer + j];
+    }
+  }
+  if (!n) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (uint32_t j = 0; j < kPer; ++j) y[j] *= inv;
+  store_out<kPer>(a, i, hq, lane * kPer, y);
+  if (a.lse && lane == 0) a.lse[id] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+template <uint32_t D, uint32_t kWarps>
+cudaError_t run_join(const AttendArgs& a, const CacheView& c, const PartsView& parts, const Division& d,
+                     cudaStream_t st) {
+  ProfRange p("attend_join", st);
+  constexpr uint32_t kRows = kJoinThreads / 32 / kWarps;
+  k_attend_join<D, kWarps><<<uint32_t((parts.rows + kRows - 1) / kRows), kJoinThreads, 0, st>>>(
+      a, c, parts, d.prefix_parts, d.splits);
+  return cudaGetLastError();
+}
 
 uint64_t parts_bytes(const AttendArgs& a, uint64_t parts) {
   const uint64_t rows = uint64_t(a.n_rows) * a.Hq;
@@ -203,10 +245,7 @@ cudaError_t run_all(const AttendArgs& a, const CacheView& c, const PartsView& pa
     if (e != cudaSuccess) return e;
   }
   if (d.parts == 1) return e;
-  ProfRange p("attend_join", st);
-  const uint64_t blocks = (parts.rows + kJoinWarps - 1) / kJoinWarps;
-  k_attend_join<D><<<uint32_t(blocks), kJoinWarps * 32, 0, st>>>(a, c, parts, d.prefix_parts, d.splits);
-  return cudaGetLastError();
+  return d.parts > 8 ? run_join<D, 8>(a, c, parts, d, st) : run_join<D, 1>(a, c, parts, d, st);
 }
 
 }  // namespace

@@ -60,6 +60,19 @@ __device__ inline bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+// Whether a phase has ended, without waiting: asked early, the answer's own
+// latency is hidden.
+__device__ inline uint32_t is_there(uint32_t bar, uint32_t parity) {
+  uint32_t there;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(there)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return there;
+}
 __device__ inline void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -390,10 +403,13 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
     const float scale = fabsf(a.scale_log2);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    uint32_t s_there = 0;
     for (uint32_t n = 0; n < turns; ++n) {
       const uint32_t b = same_rows ? 2 * n + r : n;
-      ok = await(&B.s_full[r], n & 1u);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, s_there)) {
+        ok = await(&B.s_full[r], n & 1u);
+        if (!ok) break;
+      }
       tc::fence_after_sync();
       const uint32_t base = token0 + b * T::kTokens;
       const uint32_t left = see > base ? see - base : 0u;  // tokens of the block that the row sees
@@ -434,12 +450,13 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       // a row that has seen nothing yet: its weights are zero
       const float ref = m == -INFINITY ? 0.f : -m;
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      uint32_t p[64];
+      uint32_t p[64], o_there = 0;
 #pragma unroll
       for (uint32_t i = 0; i < 64; ++i) {
         float2 e = fma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale), make_float2(ref, ref));
         e.x = ex2(e.x);
         e.y = ex2(e.y);
+        if (i == 40 && n) o_there = is_there(tc::smem_addr(&B.o_done[r]), (n - 1) & 1u);
         sum[i & 1] = add2(sum[i & 1], e);
         p[i] = pack16<DT>(e.x, e.y);
       }
@@ -454,8 +471,10 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       }
       l += add;
       if (n) {  // the product of the last P has read it, and O is complete
-        ok = await(&B.o_done[r], (n - 1) & 1u);
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, o_there)) {
+          ok = await(&B.o_done[r], (n - 1) & 1u);
+          if (!ok) break;
+        }
         tc::fence_after_sync();
         if (moves) {
 #pragma unroll
@@ -469,6 +488,7 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
           }
         }
       }
+      s_there = n + 1 < turns ? is_there(tc::smem_addr(&B.s_full[r]), (n + 1) & 1u) : 0u;
       tmem_st32(p_at, p);
       tmem_st32(p_at + 32, p + 32);
       tmem_wait_st();
@@ -519,6 +539,17 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       const uint64_t at = uint64_t(part) * parts.rows + id;
       float4* stage = reinterpret_cast<float4*>(smem + r * T::kBlock + (warp & 3u) * 4096);
       const bool writes = live && (direct || LL != -INFINITY);
+      // the rows that this lane writes channels of: 4 k + lane / 8
+      int64_t to[8];
+      uint32_t w = 0;
+      {
+        const int64_t mine = direct ? i0 * a.o_tok + int64_t(hq) * a.o_head : int64_t(at * D);
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+          to[k] = __shfl_sync(0xffffffffu, mine, k * 4 + lane / 8);
+          w |= uint32_t(__shfl_sync(0xffffffffu, uint32_t(writes), k * 4 + lane / 8)) << k;
+        }
+      }
 #pragma unroll
       for (uint32_t i = 0; i < D / 32; ++i) {
         float o[32] = {};
@@ -537,16 +568,12 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
         for (uint32_t k = 0; k < 8; ++k) {
           const uint32_t rr = k * 4 + lane / 8, u = lane & 7u;
           const float4 v = stage[rr * 8 + (u ^ (rr & 7u))];
-          const bool w = __shfl_sync(0xffffffffu, writes, rr);
-          const uint64_t to = __shfl_sync(0xffffffffu, at, rr);
-          const int32_t ti = __shfl_sync(0xffffffffu, i0, rr);
-          const uint32_t th = __shfl_sync(0xffffffffu, hq, rr);
-          if (w && direct) {
-            const float y[4] = {v.x, v.y, v.z, v.w};
-            store_out<4>(a, ti, th, 32 * i + 4 * u, y);
-          } else if (w) {
-            *reinterpret_cast<float4*>(parts.o + to * D + 32 * i + 4 * u) = v;
-          }
+          if (!(w >> k & 1u)) continue;
+          if (direct)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to[k] + 32 * i + 4 * u) =
+                make_uint2(pack16<DT>(v.x, v.y), pack16<DT>(v.z, v.w));
+          else
+            *reinterpret_cast<float4*>(parts.o + to[k] + 32 * i + 4 * u) = v;
         }
         __syncwarp();
       }
