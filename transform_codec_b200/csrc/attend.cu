@@ -152,14 +152,16 @@ Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint
     const uint64_t rows = uint64_t(std::max(max_queries, 1u)) * a.G;
     d.row_tiles = rows > 8 ? 2 : 1;
     d.row_groups = uint32_t(std::min<uint64_t>((rows + 8 * d.row_tiles - 1) / (8 * d.row_tiles), 4096u));
-    // One wave of blocks (3 an SM) is filled with parts of at least 64 tokens;
-    // with more blocks than that, parts of about 1024 tokens until there are
-    // some six waves, so that sequences of different lengths even out.
-    const uint64_t wave = kSMs * 3, blocks = uint64_t(a.n_seqs) * a.H * d.row_groups;
+    // One sequence: as many parts as fill the SMs once (4 or 3 blocks each), of at
+    // least 64 tokens. A batch: the same, or parts of about 512 tokens until there
+    // are some six waves of blocks, so that different lengths even out.
+    const uint64_t wave = kSMs * (d.row_tiles == 1 ? 4 : 3), blocks = uint64_t(a.n_seqs) * a.H * d.row_groups;
     const uint64_t fine = std::max<uint64_t>(1, (uint64_t(max_kv) + kLeastTiles * kTile - 1) / (kLeastTiles * kTile));
-    const uint64_t coarse = std::max<uint64_t>(1, uint64_t(max_kv) / 1024);
     uint64_t s = std::min(fine, std::max<uint64_t>(1, wave / std::max<uint64_t>(blocks, 1)));
-    s = std::max(s, std::min(coarse, std::max<uint64_t>(1, 6 * wave / std::max<uint64_t>(blocks, 1))));
+    if (a.n_seqs > 1) {
+      const uint64_t coarse = std::max<uint64_t>(1, uint64_t(max_kv) / 512);
+      s = std::max(s, std::min(coarse, std::max<uint64_t>(1, 6 * wave / std::max<uint64_t>(blocks, 1))));
+    }
     s = std::min<uint64_t>(s, 512);
     if (s + d.prefix_parts > 1 && s + d.prefix_parts > most) s = most > d.prefix_parts + 1 ? most - d.prefix_parts : 1;
     d.splits = uint32_t(s);

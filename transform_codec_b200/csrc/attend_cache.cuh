@@ -110,8 +110,10 @@ struct CacheTile {
   static constexpr uint32_t kScales = kKArea + kVArea;     // fp32 [k 16][v 16]
   static constexpr uint32_t kMicro = kScales + 128;        // e4m3 [k 16][D / 16], [v 16][D / 16]
   static constexpr uint32_t kStage = kMicro + (k4 ? 32 * (D / 16) : 0);
-  // 3 blocks an SM (what registers allow) keep about 200 KB in shared memory
-  static constexpr uint32_t kStages = kStage > 4000 ? 4 : kStage > 2000 ? 6 : 8;
+  // blocks an SM that registers allow; together they keep up to 200 KB on the way
+  static constexpr uint32_t kBlocks = R == 1 ? 4 : 3;
+  static constexpr uint32_t kFit = 204800 / kBlocks / kWarps / kStage;
+  static constexpr uint32_t kStages = kFit > 8 ? 8 : kFit;
   static constexpr uint32_t kRing = kWarps * kStages * kStage;
   static constexpr uint32_t kJoin = kWarps * kRows * (D + 1) * 4;  // the end's o and L of each warp
   static constexpr uint32_t kSmem = kRing > kJoin ? kRing : kJoin;
@@ -119,7 +121,7 @@ struct CacheTile {
 
 // grid (row groups * splits, H, sequences)
 template <uint32_t FMT, uint32_t D, uint32_t R>
-__global__ void __launch_bounds__(128, 3)
+__global__ void __launch_bounds__(128, (CacheTile<FMT, D, R>::kBlocks))
 k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, const uint32_t part0,
                const uint32_t splits, const uint32_t row_groups) {
   using T = CacheTile<FMT, D, R>;
