@@ -416,51 +416,65 @@ def profile_end() -> dict:
 
 
 # ---- serving cache
+#
+# A decoding step makes a handful of these calls, each a few microseconds on the
+# GPU when the batch is small, so the checks below stay cheap: plain comparisons,
+# the stream as a number, and no objects made that need not be.
 
+_torch = None
 _TORCH_DTYPES: dict = {}
+_raw_stream = None
+
+
+def _use_torch():
+    """torch, imported by the first call that needs it."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _TORCH_DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: F32})
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch = torch
+    return _torch
 
 
 def _value_type(dtype) -> int:
     """BF16, FP16 or F32 of a torch dtype; KvcError (ERR_INVALID) for another."""
-    if not _TORCH_DTYPES:
-        import torch
-        _TORCH_DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: F32})
+    _use_torch()
     dt = _TORCH_DTYPES.get(dtype)
     if dt is None:
         raise KvcError(ERR_INVALID, f"value type {dtype}")
     return dt
 
 
+def _refuse(what: str):
+    raise KvcError(ERR_INVALID, what)
+
+
 def _require(ok: bool, what: str):
     if not ok:
-        raise KvcError(ERR_INVALID, what)
+        _refuse(what)
 
 
-def _on(t, device, what: str, dtype=None):
-    """t must be a tensor of that device (and type)."""
-    if t.device != device or (dtype is not None and t.dtype != dtype):
-        raise KvcError(ERR_INVALID, f"{what}: {t.dtype} on {t.device}, not {dtype or ''} on {device}")
+def _on(t, device, what: str, dtype):
+    """t must be a tensor of that device and type."""
+    if t.device != device or t.dtype != dtype:
+        _refuse(f"{what}: {t.dtype} on {t.device}, not {dtype} on {device}")
 
 
-class _launch_on:
-    """The stream a call launches on, with the tensors' device current."""
-
-    def __init__(self, device, stream):
-        import torch
-        _require(device.type == "cuda", f"tensors on {device}")
-        self._restore = None
-        if torch.cuda.current_device() != device.index:
-            self._restore = torch.cuda.device(device)
-        self._s = torch.cuda.current_stream(device) if stream is None else stream
-
-    def __enter__(self):
-        if self._restore is not None:
-            self._restore.__enter__()
-        return self._s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._restore is not None:
-            self._restore.__exit__(*exc)
+def _launch(device, stream, what: str, fn, *args):
+    """fn(*args, stream) with the tensors' device current, on its current stream if none is given."""
+    torch = _use_torch()
+    if device.type != "cuda":
+        _refuse(f"tensors on {device}")
+    raw = _raw_stream(device.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != OK:
+        raise KvcError(status, what)
 
 
 class QuantCache:
@@ -474,7 +488,7 @@ class QuantCache:
 
     def __init__(self, fmt: int, n_heads: int, head_dim: int, page_tokens: int, n_pages: int, device=None,
                  codes=None, scales=None, micro=None):
-        import torch
+        torch = _use_torch()
         self.format, self.n_heads, self.head_dim = fmt, n_heads, head_dim
         self.page_tokens, self.n_pages = page_tokens, n_pages
         for v in (fmt, n_heads, head_dim, page_tokens, n_pages):
@@ -505,6 +519,8 @@ class QuantCache:
         self._desc.codes, self._desc.scales = self.codes.data_ptr(), self.scales.data_ptr()
         self._desc.micro = self.micro.data_ptr() if four else None
         self.ref = ctypes.byref(self._desc)
+        self._pointer = ctypes.pointer(self._desc)
+        self._res = self.res.data_ptr()
 
 
 def cache_write(cache: QuantCache, k, v, slots, res=None, stream=None):
@@ -512,19 +528,20 @@ def cache_write(cache: QuantCache, k, v, slots, res=None, stream=None):
     or f32; token and head strides free in 16-byte steps, so [head][token]
     slices go in as slices.transpose(0, 1)) into slots, int64 [n] = page *
     page_tokens + token in page, negative: skipped. Each slot at most once a call."""
-    import torch
+    torch = _torch or _use_torch()
     shape = (slots.shape[0], cache.n_heads, cache.head_dim)
-    _require(k.shape == shape and v.shape == shape, f"k {tuple(k.shape)}, v {tuple(v.shape)} for {shape}")
-    _on(k, cache.device, "k")
-    _on(v, cache.device, "v", k.dtype)
-    _on(slots, cache.device, "slots", torch.int64)
+    device, dtype = cache.device, k.dtype
+    if k.shape != shape or v.shape != shape:
+        _refuse(f"k {tuple(k.shape)}, v {tuple(v.shape)} for {shape}")
+    _on(k, device, "k", dtype)
+    _on(v, device, "v", dtype)
+    _on(slots, device, "slots", torch.int64)
     kt, kh, kc = k.stride()
     vt, vh, vc = v.stride()
-    _require(kc == 1 and vc == 1 and slots.is_contiguous(), "channels and slots are contiguous")
-    with _launch_on(cache.device, stream) as s:
-        _check(_lib.kvc_cache_write(cache.ref, _value_type(k.dtype), shape[0], k.data_ptr(), kt, kh, v.data_ptr(),
-                                    vt, vh, slots.data_ptr(), (cache.res if res is None else res).data_ptr(), s),
-               "kvc_cache_write")
+    if kc != 1 or vc != 1 or not slots.is_contiguous():
+        _refuse("channels and slots are contiguous")
+    _launch(device, stream, "kvc_cache_write", _lib.kvc_cache_write, cache.ref, _value_type(dtype), shape[0],
+            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), cache._res if res is None else res.data_ptr())
 
 
 def cache_read(cache: QuantCache, page_table, start, out_start, out, res=None, stream=None):
@@ -533,21 +550,23 @@ def cache_read(cache: QuantCache, page_table, start, out_start, out, res=None, s
     sequence the slices the codec takes) at out_start[b] .. out_start[b + 1].
     page_table int32 [n_seqs, pages], start int32 [n_seqs], out_start int32
     [n_seqs + 1]; tokens of out outside the ranges are left as they are."""
-    import torch
-    for t, what in ((page_table, "page_table"), (start, "start"), (out_start, "out_start")):
-        _on(t, cache.device, what, torch.int32)
-    _on(out, cache.device, "out")
+    torch = _torch or _use_torch()
+    device, int32 = cache.device, torch.int32
+    _on(page_table, device, "page_table", int32)
+    _on(start, device, "start", int32)
+    _on(out_start, device, "out_start", int32)
+    _on(out, device, "out", out.dtype)
     n = start.shape[0]
-    _require(page_table.dim() == 2 and page_table.shape[0] == n and out_start.shape == (n + 1,) and start.dim() == 1,
-             "page_table [n], start [n] and out_start [n + 1]")
-    _require(out.dim() == 4 and out.shape[0] == 2 and out.shape[1] == cache.n_heads
-             and out.shape[3] == cache.head_dim, f"out of shape {tuple(out.shape)}")
-    _require(page_table.is_contiguous() and start.is_contiguous() and out_start.is_contiguous()
-             and out.is_contiguous(), "contiguous tensors")
-    with _launch_on(cache.device, stream) as s:
-        _check(_lib.kvc_cache_read(cache.ref, _value_type(out.dtype), n, page_table.data_ptr(), page_table.shape[1],
-                                   start.data_ptr(), out_start.data_ptr(), out.data_ptr(), out.shape[2],
-                                   (cache.res if res is None else res).data_ptr(), s), "kvc_cache_read")
+    if page_table.dim() != 2 or page_table.shape[0] != n or out_start.shape != (n + 1,) or start.dim() != 1:
+        _refuse("page_table [n], start [n] and out_start [n + 1]")
+    if out.dim() != 4 or out.shape[0] != 2 or out.shape[1] != cache.n_heads or out.shape[3] != cache.head_dim:
+        _refuse(f"out of shape {tuple(out.shape)}")
+    if not (page_table.is_contiguous() and start.is_contiguous() and out_start.is_contiguous()
+            and out.is_contiguous()):
+        _refuse("contiguous tensors")
+    _launch(device, stream, "kvc_cache_read", _lib.kvc_cache_read, cache.ref, _value_type(out.dtype), n,
+            page_table.data_ptr(), page_table.shape[1], start.data_ptr(), out_start.data_ptr(), out.data_ptr(),
+            out.shape[2], cache._res if res is None else res.data_ptr())
 
 
 class Attention:
@@ -562,7 +581,7 @@ class Attention:
 
     def __init__(self, dtype, n_q_heads: int, n_heads: int, head_dim: int, max_rows: int, max_seqs: int,
                  max_queries: int = 1, max_kv: int = 0, prefix_tokens: int = 0, device=None):
-        import torch
+        torch = _use_torch()
         dev = torch.device("cuda") if device is None else torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
@@ -578,6 +597,7 @@ class Attention:
         self.workspace = torch.empty(max(_lib.kvc_attend_workspace_bytes(ctypes.byref(d)), 16), dtype=torch.uint8,
                                      device=dev)
         self.res = torch.zeros(2, dtype=torch.int64, device=dev)
+        self._res = self.res.data_ptr()
         self._ws, self._ws_bytes = self.workspace.data_ptr(), self.workspace.numel()
         self._ref = ctypes.byref(d)
 
@@ -597,26 +617,31 @@ class Attention:
         (k, v), each [n_heads, tokens, head_dim], tokens contiguous; prefix_len
         int32 [n_seqs] (None: all of it); lse fp32 [n, n_q_heads]; scale defaults
         to head_dim ** -0.5."""
-        import torch
-        d, dev = self._desc, self.device
-        n, heads, dim = q.shape
+        torch = _torch
+        d, dev, int32 = self._desc, self.device, torch.int32
+        n, heads, dim = shape = q.shape
         _on(q, dev, "q", self.dtype)
         _on(out, dev, "out", self.dtype)
-        _require(heads == d.n_q_heads and dim == d.head_dim and out.shape == q.shape, f"q {tuple(q.shape)}")
-        qs, os_ = q.stride(), out.stride()
-        _require(qs[2] == 1 and os_[2] == 1, "channels are contiguous")
-        seqs = None
-        for t, what, extra in ((q_start, "q_start", 1), (kv_len, "kv_len", 0), (prefix_len, "prefix_len", 0)):
-            if t is not None:
-                _on(t, dev, what, torch.int32)
-                _require(t.dim() == 1 and t.is_contiguous(), what)
-                m = t.shape[0] - extra
-                _require(m >= 0 and (seqs is None or seqs == m), f"{what} for {m} sequences")
-                seqs = m
-        d.n_rows, d.n_seqs = n, n if seqs is None else seqs
-        _require(q_start is not None or n >= d.n_seqs, "a row for each sequence")
-        d.q, d.q_token_stride, d.q_head_stride = q.data_ptr(), qs[0], qs[1]
-        d.out, d.out_token_stride, d.out_head_stride = out.data_ptr(), os_[0], os_[1]
+        if heads != d.n_q_heads or dim != d.head_dim or out.shape != shape:
+            _refuse(f"q {tuple(shape)}")
+        qt, qh, qc = q.stride()
+        ot, oh, oc = out.stride()
+        if qc != 1 or oc != 1:
+            _refuse("channels are contiguous")
+        seqs = -1
+        if q_start is not None:
+            seqs = self._sequences(q_start, "q_start", 1, seqs)
+        if kv_len is not None:
+            seqs = self._sequences(kv_len, "kv_len", 0, seqs)
+        if prefix_len is not None:
+            seqs = self._sequences(prefix_len, "prefix_len", 0, seqs)
+        if seqs < 0:
+            seqs = n
+        if q_start is None and n < seqs:
+            _refuse("a row for each sequence")
+        d.n_rows, d.n_seqs = n, seqs
+        d.q, d.q_token_stride, d.q_head_stride = q.data_ptr(), qt, qh
+        d.out, d.out_token_stride, d.out_head_stride = out.data_ptr(), ot, oh
         d.q_start = None if q_start is None else q_start.data_ptr()
         d.prefix_len = None if prefix_len is None else prefix_len.data_ptr()
         d.scale = dim ** -0.5 if scale is None else scale
@@ -624,16 +649,18 @@ class Attention:
             d.lse = None
         else:
             _on(lse, dev, "lse", torch.float32)
-            _require(lse.shape == (n, heads) and lse.is_contiguous(), f"lse {tuple(lse.shape)}")
+            if lse.shape != (n, heads) or not lse.is_contiguous():
+                _refuse(f"lse {tuple(lse.shape)}")
             d.lse = lse.data_ptr()
         if cache is None:
             d.cache, d.pages, d.kv_len = None, None, None
         else:
-            _require(cache.device == dev and page_table is not None and kv_len is not None, "cache")
-            _on(page_table, dev, "page_table", torch.int32)
-            _require(page_table.dim() == 2 and page_table.shape[0] == d.n_seqs and page_table.is_contiguous(),
-                     "page_table")
-            d.cache = ctypes.pointer(cache._desc)
+            if cache.device != dev or page_table is None or kv_len is None:
+                _refuse("cache")
+            _on(page_table, dev, "page_table", int32)
+            if page_table.dim() != 2 or page_table.shape[0] != seqs or not page_table.is_contiguous():
+                _refuse("page_table")
+            d.cache = cache._pointer
             d.pages, d.pages_stride, d.kv_len = page_table.data_ptr(), page_table.shape[1], kv_len.data_ptr()
         if prefix is None:
             d.prefix_tokens = 0
@@ -642,13 +669,21 @@ class Attention:
             _on(pk, dev, "prefix keys", self.dtype)
             _on(pv, dev, "prefix values", self.dtype)
             st = pk.stride()
-            _require(pk.dim() == 3 and pk.shape[0] == d.n_heads and pk.shape[2] == dim and pv.shape == pk.shape
-                     and st[1:] == (dim, 1) and (pv.stride() == st), f"prefix {tuple(pk.shape)}")
+            if (pk.dim() != 3 or pk.shape[0] != d.n_heads or pk.shape[2] != dim or pv.shape != pk.shape
+                    or st[1:] != (dim, 1) or pv.stride() != st):
+                _refuse(f"prefix {tuple(pk.shape)}")
             d.prefix_tokens, d.prefix_head_stride = pk.shape[1], st[0]
             d.prefix_k, d.prefix_v = pk.data_ptr(), pv.data_ptr()
-        with _launch_on(dev, stream) as s:
-            _check(_lib.kvc_attend(self._ref, self._ws, self._ws_bytes, (self.res if res is None else res).data_ptr(),
-                                   s), "kvc_attend")
+        _launch(dev, stream, "kvc_attend", _lib.kvc_attend, self._ref, self._ws, self._ws_bytes,
+                self._res if res is None else res.data_ptr())
+
+    def _sequences(self, t, what, extra, seqs):
+        """The number of sequences that t speaks of, the same as what was said before (-1: nothing yet)."""
+        _on(t, self.device, what, _torch.int32)
+        m = t.shape[0] - extra if t.dim() == 1 else -1
+        if m < 0 or (seqs >= 0 and seqs != m) or not t.is_contiguous():
+            _refuse(f"{what} {tuple(t.shape)}")
+        return m
 
 
 def stage_crc32(src, n: int, out, stream=None):
