@@ -49,52 +49,71 @@ struct Vals {
   }
 };
 
-// Quantise the 8 values x of one lane of a row of L lanes and store them at row
-// `row`. All lanes of the group take part in the shuffles; lanes past D hold zeros.
-template <uint32_t FMT, uint32_t L>
-__device__ inline void quantise_store(const CacheView& c, uint64_t row, uint32_t lane, bool live, const float* x) {
-  // largest magnitude by its bits: an infinity or NaN sorts above every number
-  uint32_t m8 = 0;
+// Largest magnitudes as bits (an infinity or NaN sorts above every number): of a
+// lane's 8 values, as a pattern of the value type. Two rows of 16-bit values go
+// through the exchange between lanes in one word.
+template <uint32_t DT>
+__device__ inline uint32_t lane_max(const Vals<DT>& v) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m8 = max(m8, __float_as_uint(x[i]) & 0x7fffffffu);
-  uint32_t mb = m8;
-  if (FMT == KVC_CACHE_E2M1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));  // block of 16 channels
-  uint32_t m = mb;
+  for (const uint4& q : v.w) {
+    constexpr uint32_t kMask = DT == KVC_DTYPE_F32 ? 0x7fffffffu : 0x7fff7fffu;
+    const uint32_t u[4] = {q.x & kMask, q.y & kMask, q.z & kMask, q.w & kMask};
 #pragma unroll
-  for (uint32_t o = FMT == KVC_CACHE_E2M1 ? 2 : 1; o < L; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const bool bad = m >= 0x7f800000u;
+    for (int i = 0; i < 4; ++i) m = DT == KVC_DTYPE_F32 ? max(m, u[i]) : __vmaxu2(m, u[i]);
+  }
+  return DT == KVC_DTYPE_F32 ? m : max(m & 0xffffu, m >> 16);
+}
+template <uint32_t DT>
+__device__ inline uint32_t max_bits(uint32_t a, uint32_t b) {
+  return DT == KVC_DTYPE_F32 ? max(a, b) : __vmaxu2(a, b);
+}
+template <uint32_t DT>
+__device__ inline float bits_f32(uint32_t m) {
+  if (DT == KVC_DTYPE_F32) return __uint_as_float(m);
+  if (DT == KVC_DTYPE_BF16) return __uint_as_float(m << 16);
+  return half2_f32(m & 0xffffu).x;
+}
+
+// Quantise one lane's 8 values x of a row and store them at row `row`; m and mb:
+// the row's and the block's largest magnitude (bits of the value type).
+template <uint32_t DT, uint32_t FMT>
+__device__ inline void quantise_store(const CacheView& c, uint64_t row, uint32_t lane, const float* x, uint32_t m,
+                                      uint32_t mb) {
   constexpr float kPeak = FMT == KVC_CACHE_E4M3 ? kE4m3Peak : FMT == KVC_CACHE_INT8 ? kInt8Peak : kE2m1Peak;
-  const float top = __uint_as_float(m);
+  const float top = bits_f32<DT>(m);
+  const bool bad = !(top < INFINITY);
   float s = 0.f, inv = 0.f;
   if (!bad && top >= kRowFloor) {
     s = top * (1.0f / kPeak);
     inv = 1.0f / s;
   }
-  if (!live) return;  // after the last shuffle
   if (lane == 0) c.scales[row] = bad ? __uint_as_float(0x7fc00000u) : s;
   if (lane * 8u >= c.D) return;
   uint8_t* dst = c.codes + row * c.row_bytes;
   if (FMT == KVC_CACHE_E2M1) {
-    const uint32_t u = e4m3x2(bad ? 0.f : (__uint_as_float(mb) * inv) * (1.0f / 6.0f), 0.f) & 0xffu;
+    const uint32_t u = e4m3x2((bits_f32<DT>(mb) * inv) * (1.0f / 6.0f), 0.f) & 0xffu;
     const float uf = e4m3_f32(u);
     const float inv_b = uf > 0.f ? 1.0f / (s * uf) : 0.f;
-    uint32_t w = 0;
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w |= e2m1x2(bad ? 0.f : x[2 * i] * inv_b, bad ? 0.f : x[2 * i + 1] * inv_b) << (8 * i);
-    *reinterpret_cast<uint32_t*>(dst + lane * 4u) = w;
-    if (!(lane & 1u)) c.micro[row * (c.D / 16u) + (lane >> 1)] = uint8_t(u);
+    for (int i = 0; i < 8; ++i) y[i] = x[i] * inv_b;
+    const uint32_t w = e2m1x8(y);
+    *reinterpret_cast<uint32_t*>(dst + lane * 4u) = bad ? 0u : w;
+    if (!(lane & 1u)) c.micro[row * (c.D / 16u) + (lane >> 1)] = bad ? uint8_t(0) : uint8_t(u);
   } else {
     uint32_t w[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = bad ? 0.f : x[4 * j + i] * inv;
+      for (int i = 0; i < 4; ++i) y[i] = x[4 * j + i] * inv;
       if (FMT == KVC_CACHE_E4M3)
         w[j] = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
       else
-        w[j] = int8_bits(y[0]) | (int8_bits(y[1]) << 8) | (int8_bits(y[2]) << 16) | (int8_bits(y[3]) << 24);
+        w[j] = __byte_perm(__byte_perm(int8_bits(y[0]), int8_bits(y[1]), 0x0040),
+                           __byte_perm(int8_bits(y[2]), int8_bits(y[3]), 0x0040), 0x5410);
+      if (bad) w[j] = 0;
     }
     *reinterpret_cast<uint2*>(dst + lane * 8u) = make_uint2(w[0], w[1]);
   }
@@ -104,33 +123,58 @@ __device__ inline void quantise_store(const CacheView& c, uint64_t row, uint32_t
 template <uint32_t DT, uint32_t FMT, uint32_t L, uint32_t U>
 __global__ void __launch_bounds__(kThreads) k_cache_write(const CacheView c, const WriteArgs a, const uint32_t t0) {
   constexpr uint32_t kGroups = kThreads / L;
+  __shared__ int64_t rows[U * kGroups];  // the tokens' cache rows, -1: none
   const uint32_t lane = threadIdx.x % L, group = threadIdx.x / L;
   const uint32_t kv = blockIdx.x >= c.H, h = blockIdx.x - kv * c.H;
+  const uint32_t tile = t0 + blockIdx.y * U * kGroups;
   const void* src = kv ? a.v : a.k;
   const int64_t ts = kv ? a.v_tok : a.k_tok, hs = kv ? a.v_head : a.k_head;
-  const uint64_t slots = uint64_t(c.n_pages) << c.page_shift;
   Vals<DT> v[U];
-  int64_t slot[U];
 #pragma unroll
   for (uint32_t u = 0; u < U; ++u) {
-    const uint32_t t = t0 + (blockIdx.y * U + u) * kGroups + group;
-    const bool in = t < a.n_tokens;
-    slot[u] = in ? __ldg(a.slots + t) : -1;
+    const uint32_t t = tile + u * kGroups + group;
     v[u].zero();
-    if (in && lane * 8u < c.D) v[u].load(src, int64_t(t) * ts + int64_t(h) * hs + lane * 8u);
+    if (t < a.n_tokens && lane * 8u < c.D) v[u].load(src, int64_t(t) * ts + int64_t(h) * hs + lane * 8u);
+  }
+  for (uint32_t i = threadIdx.x; i < U * kGroups; i += kThreads) {
+    const int64_t slot = a.n_tokens - tile > i ? __ldg(a.slots + tile + i) : -1;
+    const uint64_t page = uint64_t(slot) >> c.page_shift;
+    int64_t row = -1;
+    if (slot >= 0) {
+      if (page >= c.n_pages)
+        flag_invalid(a.res);
+      else
+        row = int64_t(cache_row(c, uint32_t(page), kv, h) + (uint64_t(slot) & c.page_mask));
+    }
+    rows[i] = row;
+  }
+  __syncthreads();
+  // magnitudes: kPair rows to a word
+  constexpr uint32_t kPair = DT == KVC_DTYPE_F32 || U == 1 ? 1 : 2;
+  uint32_t m[U], mb[U];
+#pragma unroll
+  for (uint32_t u = 0; u < U; u += kPair) {
+    uint32_t w = lane_max<DT>(v[u]);
+    if (kPair == 2) w |= lane_max<DT>(v[u + kPair - 1]) << 16;
+    if (FMT == KVC_CACHE_E2M1) w = max_bits<DT>(w, __shfl_xor_sync(0xffffffffu, w, 1));  // a block of 16 channels
+    const uint32_t wb = w;
+#pragma unroll
+    for (uint32_t o = FMT == KVC_CACHE_E2M1 ? 2 : 1; o < L; o <<= 1)
+      w = max_bits<DT>(w, __shfl_xor_sync(0xffffffffu, w, o));
+    m[u] = kPair == 2 ? w & 0xffffu : w;
+    mb[u] = kPair == 2 ? wb & 0xffffu : wb;
+    if (kPair == 2) {
+      m[u + kPair - 1] = w >> 16;
+      mb[u + kPair - 1] = wb >> 16;
+    }
   }
 #pragma unroll
   for (uint32_t u = 0; u < U; ++u) {
-    bool live = slot[u] >= 0;
-    if (live && uint64_t(slot[u]) >= slots) {
-      flag_invalid(a.res);
-      live = false;
-    }
-    const uint64_t s = live ? uint64_t(slot[u]) : 0;
-    const uint64_t row = cache_row(c, uint32_t(s >> c.page_shift), kv, h) + (s & c.page_mask);
+    const int64_t row = rows[u * kGroups + group];
+    if (row < 0) continue;
     float x[8];
     v[u].get(x);
-    quantise_store<FMT, L>(c, row, lane, live, x);
+    quantise_store<DT, FMT>(c, uint64_t(row), lane, x, m[u], mb[u]);
   }
 }
 

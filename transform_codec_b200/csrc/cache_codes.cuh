@@ -47,16 +47,20 @@ __device__ inline uint32_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ inline uint32_t e2m1x2(float lo, float hi) {
+// eight at once, y[0] in the lowest bits
+__device__ inline uint32_t e2m1x8(const float* y) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return r;
 }
-// round to nearest even, |x| <= 127 + 1/2: the low byte of x + 1.5 * 2^23
+// round to nearest even, clipped to 127: in the low byte of x + 1.5 * 2^23
 __device__ inline uint32_t int8_bits(float x) {
-  return __float_as_uint(fminf(fmaxf(x, -127.f), 127.f) + 12582912.f) & 0xffu;
+  return __float_as_uint(fminf(fmaxf(x, -127.f), 127.f) + 12582912.f);
 }
 
 // ---- codes -> half pairs (exact)
