@@ -18,6 +18,23 @@ struct Division {
   uint32_t parts;          // of a row at most
 };
 
+// A launch that may begin before this call's kernel ahead of it has ended (`behind`).
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, uint32_t threads, size_t smem, cudaStream_t st, bool behind,
+                          A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // Join the parts of each row, D / 32 channels a lane; reads parts * (D + 1) * 4
 // bytes a row. A warp takes a row, or kWarps warps its parts in turn where there
 // are many: with 64 rows of 55 parts (one query, 131,072 tokens) one warp a row
@@ -31,6 +48,7 @@ k_attend_join(const AttendArgs a, const CacheView c, const PartsView parts, cons
   __shared__ float ssum[kRows][kWarps], sy[kWarps > 1 ? kRows * kWarps : 1][D];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, part0 = warp % kWarps;
   const uint64_t id = uint64_t(blockIdx.x) * kRows + warp / kWarps;
+  await_previous();
   int32_t i = 0;
   uint32_t hq = 0, n = 0;
   if (id < parts.rows) {
@@ -115,9 +133,8 @@ cudaError_t run_join(const AttendArgs& a, const CacheView& c, const PartsView& p
                      cudaStream_t st) {
   ProfRange p("attend_join", st);
   constexpr uint32_t kRows = kJoinThreads / 32 / kWarps;
-  k_attend_join<D, kWarps><<<uint32_t((parts.rows + kRows - 1) / kRows), kJoinThreads, 0, st>>>(
-      a, c, parts, d.prefix_parts, d.splits);
-  return cudaGetLastError();
+  return launch_behind(k_attend_join<D, kWarps>, dim3(uint32_t((parts.rows + kRows - 1) / kRows)), kJoinThreads, 0, st,
+                       true, a, c, parts, d.prefix_parts, d.splits);
 }
 
 uint64_t parts_bytes(const AttendArgs& a, uint64_t parts) {
@@ -154,13 +171,13 @@ Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint
     d.row_groups = uint32_t(std::min<uint64_t>((rows + 8 * d.row_tiles - 1) / (8 * d.row_tiles), 4096u));
     // One sequence: as many parts as fill the SMs once (4 or 3 blocks each), of at
     // least 64 tokens. A batch: the same, or parts of about 512 tokens until there
-    // are some six waves of blocks, so that different lengths even out.
+    // are some four waves of blocks, so that different lengths even out.
     const uint64_t wave = kSMs * (d.row_tiles == 1 ? 4 : 3), blocks = uint64_t(a.n_seqs) * a.H * d.row_groups;
     const uint64_t fine = std::max<uint64_t>(1, (uint64_t(max_kv) + kLeastTiles * kTile - 1) / (kLeastTiles * kTile));
     uint64_t s = std::min(fine, std::max<uint64_t>(1, wave / std::max<uint64_t>(blocks, 1)));
     if (a.n_seqs > 1) {
       const uint64_t coarse = std::max<uint64_t>(1, uint64_t(max_kv) / 512);
-      s = std::max(s, std::min(coarse, std::max<uint64_t>(1, 6 * wave / std::max<uint64_t>(blocks, 1))));
+      s = std::max(s, std::min(coarse, std::max<uint64_t>(1, 4 * wave / std::max<uint64_t>(blocks, 1))));
     }
     s = std::min<uint64_t>(s, 512);
     if (s + d.prefix_parts > 1 && s + d.prefix_parts > most) s = most > d.prefix_parts + 1 ? most - d.prefix_parts : 1;
@@ -222,9 +239,8 @@ cudaError_t run_cache(const AttendArgs& a, const CacheView& c, const PartsView& 
   cudaError_t e = smem_attr(track, reinterpret_cast<const void*>(k_attend_cache<FMT, D, R>), T::kSmem);
   if (e != cudaSuccess) return e;
   ProfRange p("attend_cache", st);
-  k_attend_cache<FMT, D, R><<<dim3(d.row_groups * d.splits, a.H, a.n_seqs), T::kThreads, T::kSmem, st>>>(
-      a, c, parts, d.prefix_parts, d.splits, d.row_groups);
-  return cudaGetLastError();
+  return launch_behind(k_attend_cache<FMT, D, R>, dim3(d.row_groups * d.splits, a.H, a.n_seqs), T::kThreads, T::kSmem,
+                       st, a.prefix_tokens != 0, a, c, parts, d.prefix_parts, d.splits, d.row_groups);
 }
 template <uint32_t FMT, uint32_t D>
 cudaError_t pick_cache(const AttendArgs& a, const CacheView& c, const PartsView& parts, const Division& d,

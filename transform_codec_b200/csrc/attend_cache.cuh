@@ -19,12 +19,14 @@
 // the second is free, and is chosen such that a thread's own fragments are
 // contiguous bytes of rows: thread (g, t) = (lane / 4, lane % 4) holds token g
 // and g + 8's bytes of channel group t for S = K q', and channel group g of
-// tokens 2t, 2t + 1, 2t + 8, 2t + 9 for o = V^T w. So a thread copies the
-// bytes it will use itself, asynchronously into its own slots of a ring in
-// shared memory, several tiles ahead, and no barrier is in the loop. Each warp
-// takes every fourth tile of the block's part with a softmax of its own; the
-// four are joined at the end.
+// tokens 2t, 2t + 1, 2t + 8, 2t + 9 for o = V^T w. A warp copies its tiles in
+// whole lines, asynchronously and several tiles ahead, into a ring in shared
+// memory where each thread's bytes are together; it needs no block-wide barrier.
+// Each warp takes tiles of the block's part with a softmax of its own; the four are
+// joined at the end.
 #pragma once
+#include <type_traits>
+
 #include "attend_parts.cuh"
 
 namespace kvc {
@@ -44,7 +46,7 @@ __device__ inline void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ inline void mma16816(float* d, const uint32_t* a, const uint32_t* b) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -52,7 +54,7 @@ __device__ inline void mma16816(float* d, const uint32_t* a, const uint32_t* b) 
 }
 __device__ inline uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ inline float ex2(float x) {
@@ -63,6 +65,11 @@ __device__ inline float ex2(float x) {
 __device__ inline float lg2(float x) {
   float r;
   asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ inline float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ inline uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -110,6 +117,23 @@ struct CacheTile {
   static constexpr uint32_t kScales = kKArea + kVArea;     // fp32 [k 16][v 16]
   static constexpr uint32_t kMicro = kScales + 128;        // e4m3 [k 16][D / 16], [v 16][D / 16]
   static constexpr uint32_t kStage = kMicro + (k4 ? 32 * (D / 16) : 0);
+  // A tile's keys, and its values, lie together in memory: 512 bytes of them a copy
+  // of the warp, whole lines. Lane l's 16 bytes of copy j belong to this token, and
+  // to the slots of the thread that will use them.
+  static constexpr uint32_t kRowChunks = kRow / 16, kCopies = kRow / 32;
+  __device__ static constexpr uint32_t token(uint32_t j, uint32_t l) { return j * (32 / kRowChunks) + l / kRowChunks; }
+  __device__ static constexpr uint32_t key_slot(uint32_t j, uint32_t l) {
+    const uint32_t r = token(j, l), b = l % kRowChunks * 16;  // byte of the row
+    const uint32_t x = b / (4 * kKCopy), t = b / kKCopy % 4;
+    return (((r >> 3) * kKChunks + x) * 32 + (r & 7u) * 4 + t) * kKCopy + b % kKCopy;
+  }
+  // slots of 16 bytes by (g, t), smaller ones by (t, g): groups side by side
+  __device__ static constexpr uint32_t value_place(uint32_t g, uint32_t t) { return kVBytes == 16 ? g * 4 + t : t * 8 + g; }
+  __device__ static constexpr uint32_t value_slot(uint32_t j, uint32_t l) {
+    const uint32_t r = token(j, l), b = l % kRowChunks * 16;
+    const uint32_t i = (r & 1u) + 2 * (r >> 3), t = (r & 7u) >> 1;
+    return (i * 32 + value_place(b / kVBytes, t)) * kVBytes;
+  }
   // blocks an SM that registers allow; together they keep up to 200 KB on the way
   static constexpr uint32_t kBlocks = R == 1 ? 4 : 3;
   static constexpr uint32_t kFit = 204800 / kBlocks / kWarps / kStage;
@@ -128,59 +152,65 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
   extern __shared__ __align__(16) uint8_t smem[];
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3u;
   const uint32_t part = blockIdx.x / row_groups, h = blockIdx.y, b = blockIdx.z;
+  let_next_begin();
   const SeqRows rows = rows_of_seq(a, b);
   const uint32_t len = cache_len(a, c, b);
   const Chunks ch = chunks_of(len, splits);
   if (part >= ch.parts) return;
   const bool direct = ch.parts == 1 && !a.prefix_tokens;
-  const uint32_t tile0 = part * ch.per;
-  const uint32_t end = min(len, (tile0 + ch.per) * kTile);  // tokens of this part end here
-  const uint32_t n_tiles = end > tile0 * kTile ? (end - tile0 * kTile + kTile - 1) / kTile : 0u;
-  const uint32_t mine = n_tiles > warp ? (n_tiles - warp + T::kWarps - 1) / T::kWarps : 0u;  // this warp's tiles
+  // This warp's tiles are `first`, first + stride, ..: the blocks of a sequence walk
+  // through it side by side, so that what is read at a time lies together.
+  const uint32_t n_tiles = (len + kTile - 1) / kTile, first = part * T::kWarps + warp, stride = ch.parts * T::kWarps;
+  const uint32_t mine = first < n_tiles ? (n_tiles - 1 - first) / stride + 1 : 0u;
   const int32_t* pages = a.pages + uint64_t(b) * a.pages_stride;
   const uint64_t v_rows = uint64_t(c.H) << c.page_shift;  // from a key row to its value row
   const uint32_t ring = uint32_t(__cvta_generic_to_shared(smem)) + warp * (T::kStages * T::kStage);
+  // what this lane copies of a tile at row 0: 16 bytes of each 512, and a scale and
+  // micro-scales (lanes 0 - 15 keys, 16 - 31 values)
+  const uint8_t* codes = c.codes + lane * 16;
+  const float* scales = c.scales + (lane & 15u) + (lane >= 16 ? v_rows : 0u);
+  const uint8_t* micro = T::k4 ? c.micro + ((lane & 15u) + (lane >= 16 ? v_rows : 0u)) * (D / 16) : nullptr;
   const uint32_t total_rows = uint32_t(rows.n) * a.G;
 
   for (uint32_t group = blockIdx.x % row_groups; group * T::kRows < total_rows; group += row_groups) {
-    // ---- copies: this warp's k-th tile into stage k % kStages
-    int32_t page_of = -1;  // lane j: page of tile (k & ~31) + j
+    // ---- copies: this warp's k-th tile into the ring's next stage
+    int64_t row_of = -1;  // lane j: key row of tile (k & ~31) + j, -1: nothing to read there
+    uint32_t to_stage = 0;
+    auto copy = [&](int64_t row, uint32_t n, auto whole) {
+      constexpr bool kWhole = decltype(whole)::value;
+      const uint32_t dst = ring + to_stage * T::kStage;
+      const uint8_t* kp = codes + row * T::kRow;
+      const uint8_t* vp = kp + v_rows * T::kRow;
+#pragma unroll
+      for (uint32_t j = 0; j < T::kCopies; ++j)
+        copy_async<16>(dst + T::key_slot(j, lane), kp + j * 512, kWhole || T::token(j, lane) < n);
+#pragma unroll
+      for (uint32_t j = 0; j < T::kCopies; ++j)
+        copy_async<16>(dst + T::kKArea + T::value_slot(j, lane), vp + j * 512, kWhole || T::token(j, lane) < n);
+      copy_async<4>(dst + T::kScales + lane * 4, scales + row, kWhole || (lane & 15u) < n);
+      if constexpr (T::k4)
+        copy_async<D / 16>(dst + T::kMicro + lane * (D / 16), micro + row * (D / 16), kWhole || (lane & 15u) < n);
+    };
     auto issue = [&](uint32_t k) {
       if (k < mine) {
         if ((k & 31u) == 0) {
-          const uint32_t kk = k + lane;
-          page_of = -1;
+          const uint32_t kk = k + lane, at = (first + kk * stride) * kTile;
+          row_of = -1;
           if (kk < mine) {
-            page_of = __ldg(pages + ((uint64_t(tile0 + warp + kk * T::kWarps) * kTile) >> c.page_shift));
-            if (page_of < 0 || uint32_t(page_of) >= c.n_pages) {
+            const int32_t page = __ldg(pages + (at >> c.page_shift));
+            if (page < 0 || uint32_t(page) >= c.n_pages)
               flag_invalid(a.res);
-              page_of = -1;
-            }
+            else
+              row_of = int64_t(cache_row(c, uint32_t(page), 0, h) + (at & c.page_mask));
           }
         }
-        const int32_t page = __shfl_sync(0xffffffffu, page_of, k & 31u);
-        const uint32_t at = (tile0 + warp + k * T::kWarps) * kTile;
-        const uint32_t n = page < 0 ? 0u : min(kTile, end - at);  // tokens that are there
-        const uint64_t row = page < 0 ? 0u : cache_row(c, uint32_t(page), 0, h) + (at & c.page_mask);
-        const uint32_t dst = ring + (k % T::kStages) * T::kStage;
-        const uint8_t* kp = c.codes + row * T::kRow;
-        const uint8_t* vp = kp + v_rows * T::kRow;
-#pragma unroll
-        for (uint32_t u = 0; u < 2; ++u)  // tokens g, g + 8
-#pragma unroll
-          for (uint32_t x = 0; x < T::kKChunks; ++x)
-            copy_async<T::kKCopy>(dst + ((u * T::kKChunks + x) * 32 + lane) * T::kKCopy,
-                                  kp + (g + 8 * u) * T::kRow + (x * 4 + t) * T::kKCopy, g + 8 * u < n);
-#pragma unroll
-        for (uint32_t u = 0; u < 4; ++u) {  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-          const uint32_t tok = 2 * t + (u & 1u) + 8 * (u >> 1);
-          copy_async<T::kVBytes>(dst + T::kKArea + (u * 32 + lane) * T::kVBytes, vp + tok * T::kRow + g * T::kVBytes,
-                                 tok < n);
-        }
-        const uint64_t srow = row + (lane & 15u) + (lane >= 16 ? v_rows : 0u);
-        copy_async<4>(dst + T::kScales + lane * 4, c.scales + srow, (lane & 15u) < n);
-        if (T::k4)
-          copy_async<T::k4 ? D / 16 : 4>(dst + T::kMicro + lane * (D / 16), c.micro + srow * (D / 16), (lane & 15u) < n);
+        const int64_t row = __shfl_sync(0xffffffffu, row_of, k & 31u);
+        const uint32_t at = (first + k * stride) * kTile;
+        if (row >= 0 && at + kTile <= len)
+          copy(row, kTile, std::true_type{});
+        else  // tokens that are there, and zeros
+          copy(max(row, int64_t(0)), row < 0 ? 0u : len - at, std::false_type{});
+        if (++to_stage == T::kStages) to_stage = 0;
       }
       copy_commit();
     };
@@ -243,7 +273,7 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
       for (uint32_t j = 0; j < 2; ++j) all_see = min(all_see, lim[r][j]);
     all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, 1));
     all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, 2));
-    all_see = min(all_see, int32_t(end));
+    all_see = min(all_see, int32_t(len));
 
     float m[R][2], l[R][2], o[R][T::kSteps][4];
 #pragma unroll
@@ -254,11 +284,13 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
       for (uint32_t j = 0; j < T::kSteps; ++j) o[r][j][0] = o[r][j][1] = o[r][j][2] = o[r][j][3] = 0.f;
     }
 
+    uint32_t at_stage = 0;
     for (uint32_t k = 0; k < mine; ++k) {
       copy_wait<T::kStages - 2>();
       __syncwarp();  // the tile's scales were copied by other lanes
       issue(k + T::kStages - 1);
-      const uint8_t* st = smem + warp * (T::kStages * T::kStage) + (k % T::kStages) * T::kStage;
+      const uint8_t* st = smem + warp * (T::kStages * T::kStage) + at_stage * T::kStage;
+      if (++at_stage == T::kStages) at_stage = 0;
       const float* sc = reinterpret_cast<const float*>(st + T::kScales);
       // ---- S
       float s2[2][R][4];  // two chains of sums
@@ -315,28 +347,29 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
       }
       // ---- softmax: this thread's tokens g, g + 8 and rows 2t, 2t + 1
       const float sk[2] = {sc[g], sc[g + 8]}, sv[2] = {sc[16 + g], sc[24 + g]};
-      float lv[2], iv[2], odd[2];
+      const int32_t tok = int32_t((first + k * stride) * kTile + g);
+      const bool border = tok - int32_t(g) + int32_t(kTile) > all_see;
+      float x[R][4], iv[2];
+      bool slow = false;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const float s = fmaxf(sv[u], 0x1p-100f);  // a zero row: its codes are zero, its weight counts
-        lv[u] = lg2(s);
-        iv[u] = __fdividef(1.f, s);
-        odd[u] = sv[u] - sv[u];  // NaN for a NaN row
+        const float lv = lg2(s);
+        iv[u] = rcp(s);
+        slow |= sv[u] != sv[u];
+#pragma unroll
+        for (uint32_t r = 0; r < R; ++r)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float& v = x[r][2 * u + j];
+            v = fmaf(s2[0][r][2 * u + j] + s2[1][r][2 * u + j], sk[u] * rs[r][j], lv);
+            if (border && !(tok + 8 * u < min(lim[r][j], int32_t(len)))) v = -INFINITY;
+            slow |= v > m[r][j] + 15.f;
+          }
       }
-      const int32_t tok = int32_t((tile0 + warp + k * T::kWarps) * kTile + g);
-      const bool border = tok - int32_t(g) + int32_t(kTile) > all_see;
-      float x[R][4];
-      bool far = false;
-#pragma unroll
-      for (uint32_t r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int u = j >> 1;
-          x[r][j] = fmaf(s2[0][r][j] + s2[1][r][j], sk[u] * rs[r][j & 1], lv[u]);
-          if (border && !(tok + 8 * u < lim[r][j & 1] && tok + 8 * u < int32_t(end))) x[r][j] = -INFINITY;
-          far |= x[r][j] > m[r][j & 1] + 15.f;
-        }
-      if (__any_sync(0xffffffffu, far)) {
+      bool nans = false;  // a value row is NaN
+      if (__any_sync(0xffffffffu, slow)) {
+        nans = __any_sync(0xffffffffu, sv[0] != sv[0] || sv[1] != sv[1]);
 #pragma unroll
         for (uint32_t r = 0; r < R; ++r)
 #pragma unroll
@@ -364,13 +397,13 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
           const bool hidden = border && x[r][j] == -INFINITY;
           const float w = hidden ? 0.f : ex2(x[r][j] - m[r][j & 1]);
           l[r][j & 1] = fmaf(w, iv[j >> 1], l[r][j & 1]);
-          x[r][j] = hidden ? 0.f : w + odd[j >> 1];
+          x[r][j] = nans && !hidden && sv[j >> 1] != sv[j >> 1] ? sv[j >> 1] : w;
         }
         pw[r][0] = transpose8x8(pack_half(x[r][0], x[r][1]));
         pw[r][1] = transpose8x8(pack_half(x[r][2], x[r][3]));
       }
       // ---- o: channel group g of tokens 2t, 2t + 1 | 2t + 8, 2t + 9
-      const uint8_t* vs = st + T::kKArea + lane * T::kVBytes;
+      const uint8_t* vs = st + T::kKArea + T::value_place(g, t) * T::kVBytes;
       uint32_t vw[4][T::kVBytes / 4];
 #pragma unroll
       for (uint32_t u = 0; u < 4; ++u) {
@@ -492,6 +525,7 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
     }
     __syncthreads();
   }
+  await_previous();
 }
 
 }  // namespace

@@ -20,6 +20,13 @@ struct PartsView {
   uint64_t rows;  // n_rows * Hq
 };
 
+// The kernels of one call follow one another without a gap: each lets the next
+// begin once all its blocks run, and waits for the one before only where it needs
+// it done: the join before it reads, the cache kernel (which needs nothing of the
+// prefix kernel's) before it ends, so that the join's wait for it covers both.
+__device__ inline void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ inline void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Sequence b's query rows; a range that is not within the rows given is refused.
 struct SeqRows {
   int32_t first, n;

@@ -201,6 +201,7 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
   const bool same_rows = total_rows <= T::kRows;  // both tiles hold the same rows
   const uint64_t row0 = uint64_t(blockIdx.x / n_parts) * (2 * T::kRows);
 
+  let_next_begin();
   if (tid == 0) {
     for (uint32_t i = 0; i < 4; ++i) {
       tc::mbar_init(&B.k_full[i], 1);
