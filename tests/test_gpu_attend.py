@@ -215,6 +215,65 @@ def test_a_sequence_s_share_hides_what_others_see():
     assert torch.equal(out[0], clean[0]) and torch.isnan(out[1]).all()
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-40, 3.0])
+def test_unusual_scales(scale):
+    """Negative scales turn the order round, a scale of zero weighs all tokens alike."""
+    host = HostCache(kvc.CACHE_E2M1, 2, 128, 16, [50, 3], seed=2)
+    q = _randn(3, 5, 8, 128, dt=torch.float16, spread=0.5)
+    prefix = tuple(_randn(s, 2, 200, 128, dt=torch.float16) for s in (1, 2))
+    _run(host, q, [0, 4, 5], prefix, [130, 0], scale=scale)
+    _run(host, q, [0, 4, 5], scale=scale)
+
+
+def test_prefix_that_no_one_shares():
+    q = _randn(5, 3, 8, 128, dt=torch.bfloat16)
+    prefix = tuple(_randn(s, 1, 300, 128, dt=torch.bfloat16) for s in (1, 2))
+    out, lse = _run(None, q, [0, 1, 2, 3], prefix, [0, 0, 0])
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    q = _randn(5, 100, 8, 128, dt=torch.bfloat16)  # more rows than one block takes
+    out, lse = _run(None, q, [0, 50, 100], prefix, [0, 0])
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite_stay_in_their_rows(what):
+    host = HostCache(kvc.CACHE_E4M3, 1, 128, 16, [70, 5], seed=2)
+    prefix = tuple(_randn(s, 1, 200, 128, dt=torch.bfloat16) for s in (1, 2))
+    q = _randn(3, 2, 8, 128, dt=torch.bfloat16)
+    for kw in (dict(host=host), dict(host=None, prefix=prefix), dict(host=host, prefix=prefix)):
+        clean, _ = _run(q=q, starts=[0, 1, 2], **kw)
+        bad = q.clone()
+        bad[0, 3, 17] = what
+        out, lse = _run(q=bad, starts=[0, 1, 2], check=False, **kw)
+        assert torch.isnan(out[0, 3]).all()
+        keep = torch.ones(2, 8, dtype=torch.bool)
+        keep[0, 3] = False
+        assert torch.equal(out[keep.cuda()], clean[keep.cuda()])
+
+
+def test_zero_queries_weigh_all_tokens_alike():
+    host = HostCache(kvc.CACHE_INT8, 2, 64, 16, [33], seed=2)
+    _run(host, torch.zeros(1, 4, 64, dtype=torch.float16), [0, 1])
+
+
+def test_large_and_tiny_queries():
+    """Magnitudes near bf16's ends: the score's scale is kept apart from the elements."""
+    host = HostCache(kvc.CACHE_INT8, 1, 64, 16, [40], seed=2)
+    for size in (2.0 ** 100, 2.0 ** -100):
+        q = _randn(3, 1, 4, 64, dt=torch.bfloat16) * size
+        _run(host, q, [0, 1], scale=1.0 / size)
+
+
+def test_many_sequences():
+    """More sequences than any one wave of blocks, most of them short, some empty."""
+    lens = [(i * 37) % 90 for i in range(700)]
+    host = HostCache(kvc.CACHE_E4M3, 1, 64, 16, lens, seed=2)
+    q = _randn(3, 700, 2, 64, dt=torch.bfloat16)
+    _run(host, q, list(range(701)))
+    prefix = tuple(_randn(s, 1, 140, 64, dt=torch.bfloat16) for s in (1, 2))
+    _run(host, q, list(range(701)), prefix, [(i * 13) % 141 for i in range(700)])
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_hints_and_workspace_do_not_change_results_beyond_rounding(fmt):
     """Wrong expectations of the largest sequence, and the least workspace."""
@@ -227,9 +286,13 @@ def test_hints_and_workspace_do_not_change_results_beyond_rounding(fmt):
         _run(host, q, [0, 3, 4, 10], max_queries=mq, max_kv=mk)
     att = kvc.Attention(q.dtype, 8, 2, 64, max_rows=15, max_seqs=3, max_queries=6, max_kv=2000, prefix_tokens=700)
     least = kvc.lib().kvc_attend_workspace_min(att._ref)
-    assert least <= att._ws_bytes
+    assert 0 < least <= att._ws_bytes
     att._ws_bytes = least
     _run(host, q, [0, 3, 4, 10], prefix, att=att)
+    att._ws_bytes = least - 1
+    with pytest.raises(kvc.KvcError) as e:
+        _run(host, q, [0, 3, 4, 10], prefix, att=att)
+    assert e.value.status == kvc.ERR_CAPACITY
 
 
 def test_strided_queries_and_outputs():

@@ -147,6 +147,19 @@ def test_unsupported_head_dims():
     assert {v for k, v in got.items() if k.startswith(("min", "best"))} == {0}
 
 
+CAPACITY = r'''
+attend("no workspace", ws=None, ws_bytes=0)
+attend("one byte short", ws_bytes=2 * 4 * 8 * 4 * (64 + 1) - 1)   # two parts of every row: o and L
+'''
+
+
+def test_workspace_below_the_least():
+    got = _calls(CAPACITY)
+    assert {v for k, v in got.items() if k.startswith("attend")} == {kvc.ERR_CAPACITY}
+    assert {v for k, v in got.items() if k.startswith("min")} == {2 * 4 * 8 * 4 * (64 + 1)}
+    assert all(v > 2 * 4 * 8 * 4 * (64 + 1) for k, v in got.items() if k.startswith("best"))
+
+
 def test_empty_calls_launch_nothing():
     got = _calls(FINE)
     assert {v for k, v in got.items() if not k.startswith(("min", "best"))} == {kvc.OK}
