@@ -149,15 +149,18 @@ Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint
     const uint64_t rows = uint64_t(a.n_rows) * a.G, room = most > uint64_t(a.has_cache) ? most - a.has_cache : 1;
     const uint32_t nb = a.prefix_tokens / 128 + (a.prefix_tokens % 128 != 0);
     const uint64_t units = (rows + 255) / 256 * a.H;
-    // Estimated time of n parts: waves of blocks (one an SM, 2 us to begin and
-    // end) of so many 128-token steps each (1.4 us for two tiles of rows, 0.8
-    // for one), and writing and reading back n results a row at 4 KB a ns.
-    const double step = rows <= 128 ? 0.8 : 1.4, result = double(rows) * a.H * a.D * 8.0 / 4e6;
+    // Time of n parts as measured: waves of blocks (one an SM), each 12 us and 0.71
+    // a 128-token block for up to 128 rows, 19 us and 1.4 for two tiles of rows, and
+    // n results a row written and joined at 1.9 KB a ns. (8192 tokens for 128 rows of
+    // 8 heads: 1 part 66 us, 4 33, 8 29, 16 33, 32 45 with the call's other kernels;
+    // 32,768 for 1024 rows: 1 part 406, 4 144, 9 168, 13 180.)
+    const double step = rows <= 128 ? 0.71 : 1.4, begin = rows <= 128 ? 12.0 : 19.0,
+                 result = double(rows) * a.H * a.D * 8.0 / 1.9e6;
     double best = 0.0;
     for (uint32_t n = 1; n <= std::min<uint64_t>({nb, room, 256}); ++n) {
       const uint32_t per = (nb + n - 1) / n;
       if (n > 1 && (nb + per - 1) / per != n) continue;
-      const double cost = double((units * n + kSMs - 1) / kSMs) * (2.0 + per * step) + n * result;
+      const double cost = double((units * n + kSMs - 1) / kSMs) * (begin + per * step) + n * result;
       if (n == 1 || cost < best) {
         best = cost;
         d.prefix_parts = n;
