@@ -24,6 +24,11 @@
 // memory where each thread's bytes are together; it needs no block-wide barrier.
 // Each warp takes tiles of the block's part with a softmax of its own; the four are
 // joined at the end.
+//
+// Measured: 131,072 tokens of 8 heads x 128 in int8 for one query, 277 MB, 61 us (4.5
+// TB/s; 42 us at the measured 6.56; the loads alone take 58). 4-bit codes are bound
+// by instructions: 411 a tile and warp, 61% of issue slots, 64 sequences with 321 MB
+// in 93 us. With more than 16 query rows a sequence each 16 take the codes again.
 #pragma once
 #include <type_traits>
 
