@@ -37,8 +37,8 @@ cudaError_t launch_behind(void (*kern)(P...), dim3 grid, uint32_t threads, size_
 
 // Join the parts of each row, D / 32 channels a lane; reads parts * (D + 1) * 4
 // bytes a row. A warp takes a row, or kWarps warps its parts in turn where there
-// are many: with 64 rows of 55 parts (one query, 131,072 tokens) one warp a row
-// spent 59 us on loads one after another, eight spend 5.
+// are many: with 64 rows of 128 parts (one query, 131,072 tokens) one warp a row
+// spent 59 us on loads one after another, eight spent 8 (and 4 on 74 parts).
 constexpr uint32_t kJoinThreads = 256;
 template <uint32_t D, uint32_t kWarps>
 __global__ void __launch_bounds__(kJoinThreads)
