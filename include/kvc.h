@@ -466,6 +466,10 @@ int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, cons
  *                  prefix_head_stride values apart
  *   d_prefix_len   device [n_seqs]: how many of the prefix's tokens sequence b
  *                  sees; NULL: all
+ *                  Prefix values are finite up to the longest share: one that is
+ *                  not may reach rows that do not see its token (a weight of zero
+ *                  times it). Keys, and everything behind the longest share, may
+ *                  hold anything.
  * A row that sees nothing gets zeros and lse = -infinity. Rows outside
  * [d_q_start[0], d_q_start[n_seqs]) are left as they are.
  * kvc_attend_workspace_bytes is the workspace at which the work is split best;

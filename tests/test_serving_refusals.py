@@ -198,7 +198,11 @@ def test_binding_refuses_tensors():
     bad = [lambda: kvc.cache_write(c, k[:2], k, slots), lambda: kvc.cache_write(c, k, k.float(), slots),
            lambda: kvc.cache_write(c, k, k, slots.int()), lambda: kvc.cache_write(c, k[:, :1], k[:, :1], slots),
            lambda: kvc.cache_write(c, k.transpose(1, 2).contiguous().transpose(1, 2), k, slots),
-           lambda: kvc.cache_write(c, k.to("meta"), k, slots),
+           lambda: kvc.cache_write(c, k.to("meta"), k, slots), lambda: kvc.cache_write(c, k, k, slots[:, None]),
+           lambda: kvc.cache_write(c, k, k, slots[0]), lambda: kvc.cache_write(c, k, k, slots),  # tensors on the CPU
+           lambda: kvc.cache_read(c, i(0, 1)[None], i(0)[0], i(0, 5), out),
+           lambda: kvc.cache_read(c, i(0, 1)[None], i(0), i(0, 5), out),
+           lambda: kvc.cache_read(c, i(0, 1)[None], i(0), i(0, 5), out.double()),
            lambda: kvc.cache_read(c, i(0, 1), i(0), i(0, 5), out),
            lambda: kvc.cache_read(c, i(0, 1)[None], i(0), i(0, 5, 6), out),
            lambda: kvc.cache_read(c, i(0, 1)[None].long(), i(0), i(0, 5), out),
@@ -220,7 +224,8 @@ def test_binding_refuses_tensors():
     q, o = torch.zeros(4, 8, 64, dtype=torch.bfloat16), torch.zeros(4, 8, 64, dtype=torch.bfloat16)
     table, lens = torch.zeros(4, 4, dtype=torch.int32), i(1, 2, 3, 4)
     p = torch.zeros(2, 9, 64, dtype=torch.bfloat16)
-    runs = [dict(q=q.half()), dict(out=o[:3]), dict(q=q[:, :4], out=o[:, :4]), dict(kv_len=i(1, 2)),
+    runs = [dict(q=q[0], out=o[0]), dict(), dict(q=q.half()), dict(out=o[:3]), dict(q=q[:, :4], out=o[:, :4]),
+            dict(kv_len=i(1, 2)),
             dict(kv_len=lens.long()), dict(page_table=table[:2]), dict(page_table=None), dict(q_start=i(0, 1, 2)),
             dict(prefix=(p, p[:, :5])), dict(prefix=(p.transpose(1, 2), p.transpose(1, 2))),
             dict(prefix=(p[:1], p[:1])), dict(prefix_len=i(1)), dict(lse=torch.zeros(4, 4)),

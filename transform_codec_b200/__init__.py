@@ -529,6 +529,8 @@ def cache_write(cache: QuantCache, k, v, slots, res=None, stream=None):
     slices go in as slices.transpose(0, 1)) into slots, int64 [n] = page *
     page_tokens + token in page, negative: skipped. Each slot at most once a call."""
     torch = _torch or _use_torch()
+    if slots.dim() != 1:
+        _refuse(f"slots {tuple(slots.shape)}")
     shape = (slots.shape[0], cache.n_heads, cache.head_dim)
     device, dtype = cache.device, k.dtype
     if k.shape != shape or v.shape != shape:
@@ -556,7 +558,7 @@ def cache_read(cache: QuantCache, page_table, start, out_start, out, res=None, s
     _on(start, device, "start", int32)
     _on(out_start, device, "out_start", int32)
     _on(out, device, "out", out.dtype)
-    n = start.shape[0]
+    n = start.numel()
     if page_table.dim() != 2 or page_table.shape[0] != n or out_start.shape != (n + 1,) or start.dim() != 1:
         _refuse("page_table [n], start [n] and out_start [n + 1]")
     if out.dim() != 4 or out.shape[0] != 2 or out.shape[1] != cache.n_heads or out.shape[3] != cache.head_dim:
@@ -619,7 +621,10 @@ class Attention:
         to head_dim ** -0.5."""
         torch = _torch
         d, dev, int32 = self._desc, self.device, torch.int32
-        n, heads, dim = shape = q.shape
+        shape = q.shape
+        if len(shape) != 3:
+            _refuse(f"q {tuple(shape)}")
+        n, heads, dim = shape
         _on(q, dev, "q", self.dtype)
         _on(out, dev, "out", self.dtype)
         if heads != d.n_q_heads or dim != d.head_dim or out.shape != shape:

@@ -133,7 +133,9 @@ struct CacheTile {
     return (((r >> 3) * kKChunks + x) * 32 + (r & 7u) * 4 + t) * kKCopy + b % kKCopy;
   }
   // slots of 16 bytes by (g, t), smaller ones by (t, g): groups side by side
-  __device__ static constexpr uint32_t value_place(uint32_t g, uint32_t t) { return kVBytes == 16 ? g * 4 + t : t * 8 + g; }
+  __device__ static constexpr uint32_t value_place(uint32_t g, uint32_t t) {
+    return kVBytes == 16 ? g * 4 + t : t * 8 + g;
+  }
   __device__ static constexpr uint32_t value_slot(uint32_t j, uint32_t l) {
     const uint32_t r = token(j, l), b = l % kRowChunks * 16;
     const uint32_t i = (r & 1u) + 2 * (r >> 3), t = (r & 7u) >> 1;

@@ -258,7 +258,8 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       const int64_t at = __shfl_sync(0xffffffffu, src, from);
       const bool used = __shfl_sync(0xffffffffu, see, from) != 0;
       w[i] = make_uint4(0, 0, 0, 0);
-      if (used) w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + lane % kLanes * 8));
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + at + lane % kLanes * 8;
+      if (used) w[i] = __ldg(reinterpret_cast<const uint4*>(p));
     }
 #pragma unroll
     for (uint32_t i = 0; i < 32 / kAtOnce; ++i) {
@@ -281,125 +282,127 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
   };
 
   if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-  if (warp == 8 || warp == 11) {
-    // ---- loads: K blocks, V blocks
-    const bool is_v = warp == 11;
-    const uint32_t stages = is_v ? T::kVStages : T::kKStages;
-    uint64_t* full = is_v ? B.v_full : B.k_full;
-    uint64_t* empty = is_v ? B.v_empty : B.k_empty;
-    uint8_t* ring = smem + (is_v ? T::kV : T::kK);
-    uint32_t b = 0;
-    if (lane == 0) {
-      const CUtensorMap* map = is_v ? &vmap : &kmap;
-      for (; b < nb; ++b) {
-        const uint32_t s = b % stages, use = b / stages;
-        if (use && !wait_or_stop(tc::smem_addr(&empty[s]), (use - 1) & 1u, stop)) {
-          *stop = 1;
-          break;
-        }
-        const uint32_t dst = tc::smem_addr(ring + s * T::kBlock);
-        mbar_expect(&full[s], T::kBlock);
-#pragma unroll
-        for (uint32_t x = 0; x < D / 64; ++x)
-          tma_load3(dst + x * T::kHalf, map, int32_t(x * 64), int32_t(token0 + b * T::kTokens), int32_t(h), &full[s]);
-      }
-      // what was issued lands before the block leaves, also after a stop
-      for (uint32_t i = b > stages ? b - stages : 0; i < b; ++i)
-        tc::mbar_wait(&full[i % stages], (i / stages) & 1u, kDrainPolls);
-    }
-    b = __shfl_sync(0xffffffffu, b, 0);
-    const uint32_t first = (seen - token0) % T::kTokens;
-    if (is_v && b == nb && nb && first) {
-      // tokens of the last block that no row of this block sees may hold anything;
-      // their weights are zero, and so must be what they multiply
-      const uint32_t n = (T::kTokens - first) * 8;
-      uint8_t* v = ring + (nb - 1) % stages * T::kBlock;
-      for (uint32_t i = lane; i < n * (D / 64); i += 32)
-        *reinterpret_cast<uint4*>(v + (i / n) * T::kHalf + first * 128 + (i % n) * 16) = make_uint4(0, 0, 0, 0);
-      tc::fence_async_smem();
-      mbar_arrive(&B.tail);
-    }
-  } else if (nb) {
-    // ---- products: one warp issues Q K^T, the other P V. The issue of a product
-    // waits for the tensor pipe, a few products deep, and a wait for a barrier that
-    // is already there still takes some 200 clocks: with one warp for both the
-    // pipe ran dry in between. One lane issues, the whole warp walks along, so that
-    // operands are uniform.
-    bool ok = true;
-    uint32_t stage = 0, phase = 0;  // of the warp's next block
-    auto await_u = [&](uint32_t bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop)) != 0;
-      return ok;
-    };
-    if (warp == 9) {
-      const uint32_t s_desc = idesc_16(kBf16, 128, 128, false);
-      const uint64_t q0 = tc::desc_sw128(tc::smem_addr(smem)), k0 = tc::desc_sw128(tc::smem_addr(smem + T::kK));
-      const uint32_t full0 = tc::smem_addr(&B.k_full[0]), empty0 = tc::smem_addr(&B.k_empty[0]),
-                     s_full0 = tc::smem_addr(&B.s_full[0]), s_free = tc::smem_addr(&B.s_free);
-      // One S at a time stands in tensor memory: the next may come once the last has
-      // been taken to registers. So the S of a tile is there when its softmax
-      // returns from the one before.
-      const uint32_t items = same_rows ? nb : 2 * nb;
-      for (uint32_t it = 0; it < items; ++it) {
-        const uint32_t t = it & 1u;
-        const bool takes = same_rows || !t, frees = same_rows || t;
-        if (takes) await_u(full0 + stage * 8, phase);
-        if (it) await_u(s_free, (it - 1) & 1u);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint64_t q = q0 + t * (T::kBlock >> 4), k = k0 + stage * (T::kBlock >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (uint32_t s = 0; s < D / 16; ++s) {
-            const uint32_t off = ((s / 4) * T::kHalf + (s % 4) * 32) >> 4;
-            tc::mma_bf16(tmem, q + off, k + off, s_desc, s != 0);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 8 || warp == 11) {
+      // ---- loads: K blocks, V blocks
+      const bool is_v = warp == 11;
+      const uint32_t stages = is_v ? T::kVStages : T::kKStages;
+      uint64_t* full = is_v ? B.v_full : B.k_full;
+      uint64_t* empty = is_v ? B.v_empty : B.k_empty;
+      uint8_t* ring = smem + (is_v ? T::kV : T::kK);
+      uint32_t b = 0;
+      if (lane == 0) {
+        const CUtensorMap* map = is_v ? &vmap : &kmap;
+        for (; b < nb; ++b) {
+          const uint32_t s = b % stages, use = b / stages;
+          if (use && !wait_or_stop(tc::smem_addr(&empty[s]), (use - 1) & 1u, stop)) {
+            *stop = 1;
+            break;
           }
-          commit(s_full0 + t * 8);
-          if (frees) commit(empty0 + stage * 8);
-        }
-        if (frees && ++stage == T::kKStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    } else {
-      const uint32_t o_desc = idesc_16(kBf16, 128, D, true);
-      const uint64_t v0 = desc_mn_sw128(tc::smem_addr(smem + T::kV), T::kHalf);
-      const uint32_t full0 = tc::smem_addr(&B.v_full[0]), empty0 = tc::smem_addr(&B.v_empty[0]),
-                     p_full0 = tc::smem_addr(&B.p_full[0]), o_done0 = tc::smem_addr(&B.o_done[0]);
-      const bool tail = (seen - token0) % T::kTokens != 0;
-      const uint32_t items = same_rows ? nb : 2 * nb;
-      for (uint32_t it = 0; it < items; ++it) {
-        const uint32_t t = it & 1u, turn = it >> 1;
-        const bool takes = same_rows || !t, frees = same_rows || t;
-        if (takes) {
-          await_u(full0 + stage * 8, phase);
-          if (tail && (same_rows ? it : turn) + 1 == nb) await_u(tc::smem_addr(&B.tail), 0);
-        }
-        await_u(p_full0 + t * 8, turn & 1u);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint64_t v = v0 + stage * (T::kBlock >> 4);
-        if (elect_one()) {
+          const uint32_t dst = tc::smem_addr(ring + s * T::kBlock);
+          mbar_expect(&full[s], T::kBlock);
 #pragma unroll
-          for (uint32_t s = 0; s < T::kTokens / 16; ++s)
-            mma_ts(tmem + T::kO + t * D, tmem + T::kP + t * 64 + s * 8, v + s * (2048 >> 4), o_desc, turn != 0 || s != 0);
-          commit(o_done0 + t * 8);
-          if (frees) commit(empty0 + stage * 8);
+          for (uint32_t x = 0; x < D / 64; ++x)
+            tma_load3(dst + x * T::kHalf, map, int32_t(x * 64), int32_t(token0 + b * T::kTokens), int32_t(h), &full[s]);
         }
-        if (frees && ++stage == T::kVStages) {
-          stage = 0;
-          phase ^= 1u;
+        // what was issued lands before the block leaves, also after a stop
+        for (uint32_t i = b > stages ? b - stages : 0; i < b; ++i)
+          tc::mbar_wait(&full[i % stages], (i / stages) & 1u, kDrainPolls);
+      }
+      __syncwarp();
+      b = __shfl_sync(0xffffffffu, b, 0);
+      const uint32_t first = (seen - token0) % T::kTokens;
+      if (is_v && b == nb && nb && first) {
+        // tokens of the last block that no row of this block sees may hold anything;
+        // their weights are zero, and so must be what they multiply
+        const uint32_t n = (T::kTokens - first) * 8;
+        uint8_t* v = ring + (nb - 1) % stages * T::kBlock;
+        for (uint32_t i = lane; i < n * (D / 64); i += 32)
+          *reinterpret_cast<uint4*>(v + (i / n) * T::kHalf + first * 128 + (i % n) * 16) = make_uint4(0, 0, 0, 0);
+        tc::fence_async_smem();
+        mbar_arrive(&B.tail);
+      }
+    } else if (nb) {
+      // ---- products: one warp issues Q K^T, the other P V. The issue of a product
+      // waits for the tensor pipe, a few products deep, and a wait for a barrier that
+      // is already there still takes some 200 clocks: with one warp for both the
+      // pipe ran dry in between. One lane issues, the whole warp walks along, so that
+      // operands are uniform.
+      bool ok = true;
+      uint32_t stage = 0, phase = 0;  // of the warp's next block
+      auto await_u = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop)) != 0;
+        return ok;
+      };
+      if (warp == 9) {
+        const uint32_t s_desc = idesc_16(kBf16, 128, 128, false);
+        const uint64_t q0 = tc::desc_sw128(tc::smem_addr(smem)), k0 = tc::desc_sw128(tc::smem_addr(smem + T::kK));
+        const uint32_t full0 = tc::smem_addr(&B.k_full[0]), empty0 = tc::smem_addr(&B.k_empty[0]),
+                       s_full0 = tc::smem_addr(&B.s_full[0]), s_free = tc::smem_addr(&B.s_free);
+        // One S at a time stands in tensor memory: the next may come once the last has
+        // been taken to registers. So the S of a tile is there when its softmax
+        // returns from the one before.
+        const uint32_t items = same_rows ? nb : 2 * nb;
+        for (uint32_t it = 0; it < items; ++it) {
+          const uint32_t t = it & 1u;
+          const bool takes = same_rows || !t, frees = same_rows || t;
+          if (takes) await_u(full0 + stage * 8, phase);
+          if (it) await_u(s_free, (it - 1) & 1u);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t q = q0 + t * (T::kBlock >> 4), k = k0 + stage * (T::kBlock >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (uint32_t s = 0; s < D / 16; ++s) {
+              const uint32_t off = ((s / 4) * T::kHalf + (s % 4) * 32) >> 4;
+              tc::mma_bf16(tmem, q + off, k + off, s_desc, s != 0);
+            }
+            commit(s_full0 + t * 8);
+            if (frees) commit(empty0 + stage * 8);
+          }
+          if (frees && ++stage == T::kKStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      } else {
+        const uint32_t o_desc = idesc_16(kBf16, 128, D, true);
+        const uint64_t v0 = desc_mn_sw128(tc::smem_addr(smem + T::kV), T::kHalf);
+        const uint32_t full0 = tc::smem_addr(&B.v_full[0]), empty0 = tc::smem_addr(&B.v_empty[0]),
+                       p_full0 = tc::smem_addr(&B.p_full[0]), o_done0 = tc::smem_addr(&B.o_done[0]);
+        const bool tail = (seen - token0) % T::kTokens != 0;
+        const uint32_t items = same_rows ? nb : 2 * nb;
+        for (uint32_t it = 0; it < items; ++it) {
+          const uint32_t t = it & 1u, turn = it >> 1;
+          const bool takes = same_rows || !t, frees = same_rows || t;
+          if (takes) {
+            await_u(full0 + stage * 8, phase);
+            if (tail && (same_rows ? it : turn) + 1 == nb) await_u(tc::smem_addr(&B.tail), 0);
+          }
+          await_u(p_full0 + t * 8, turn & 1u);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t v = v0 + stage * (T::kBlock >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (uint32_t s = 0; s < T::kTokens / 16; ++s)
+              mma_ts(tmem + T::kO + t * D, tmem + T::kP + t * 64 + s * 8, v + s * (2048 >> 4), o_desc,
+                   turn != 0 || s != 0);
+            commit(o_done0 + t * 8);
+            if (frees) commit(empty0 + stage * 8);
+          }
+          if (frees && ++stage == T::kVStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
+      if (!ok) *stop = 1;
+      // all products have ended before tensor memory is given back, also after a stop
+      if (elect_one()) commit(tc::smem_addr(&B.drain[warp - 9]));
+      tc::mbar_wait(&B.drain[warp - 9], 0, kDrainPolls);
+      __syncwarp();
     }
-    if (!ok) *stop = 1;
-    // all products have ended before tensor memory is given back, also after a stop
-    if (elect_one()) commit(tc::smem_addr(&B.drain[warp - 9]));
-    tc::mbar_wait(&B.drain[warp - 9], 0, kDrainPolls);
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax of row `my` of tile r
@@ -439,7 +442,6 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
       for (uint32_t i = 12; i < 124; i += 8)
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) top[j] = max3(top[j], x[i + j], x[i + 4 + j]);
-      // (x[124 .. 127] are left)
 #pragma unroll
       for (uint32_t j = 0; j < 4; ++j) top[j] = max3(top[j], x[124 + j], x[124 + j]);
       float high = max3(max3(top[0], top[1], top[2]), top[3], top[3]) * scale;
