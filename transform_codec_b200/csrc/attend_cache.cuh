@@ -8,12 +8,18 @@
 // padding. Codes are exact in fp16 whatever their format, so
 //     S[token][row] = s_k (c_k . q'),  q' = q 2^e (e: the row's largest element to [2^7, 2^8)),
 // is exact up to fp32 sums. For the second product the value scale goes into the weight,
-//     w = 2^(S + log2 s_v - m),   o = sum w c_v,   l = sum w / s_v,
+//     w = 2^(S + log2 s_v - m),   o = sum w c_v,
 // with m a running reference, 7 below the largest S + log2 s_v when it was set:
 // the largest weight is 2^7 or more, so that fp16 leaves weights 2^-32 of it
-// their place, and attention on a row of tiny values keeps its bits. m moves
-// only when a score passes it by 15 (weights up to 2^15 are as exact), so the
-// usual tile needs no exchange between lanes but one vote.
+// their place, and attention on rows of tiny values keeps its bits. The sum of
+// exponentials has a reference of its own,
+//     l = sum 2^(S - n),   answer = o 2^(m - n) / l,
+// so that a token's share of it does not depend on how large its values are: a
+// row of zeros beside rows of 2^100 counts like any other. (Summing w / s_v saves
+// that exponential, 3 to 5% of the time, and loses tokens whose scale is 2^-126 of
+// the largest.) m and n move only
+// when passed by 15 (weights up to 2^15 are as exact), so the usual tile needs no
+// exchange between lanes but one vote.
 //
 // Layout: the order of channels within the first product and of tokens within
 // the second is free, and is chosen such that a thread's own fragments are
@@ -70,11 +76,6 @@ __device__ inline float ex2(float x) {
 __device__ inline float lg2(float x) {
   float r;
   asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ inline float rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ inline uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -282,10 +283,10 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
     all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, 2));
     all_see = min(all_see, int32_t(len));
 
-    float m[R][2], l[R][2], o[R][T::kSteps][4];
+    float m[R][2], n[R][2], l[R][2], o[R][T::kSteps][4];
 #pragma unroll
     for (uint32_t r = 0; r < R; ++r) {
-      m[r][0] = m[r][1] = -INFINITY;
+      m[r][0] = m[r][1] = n[r][0] = n[r][1] = -INFINITY;
       l[r][0] = l[r][1] = 0.f;
 #pragma unroll
       for (uint32_t j = 0; j < T::kSteps; ++j) o[r][j][0] = o[r][j][1] = o[r][j][2] = o[r][j][3] = 0.f;
@@ -356,39 +357,41 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
       const float sk[2] = {sc[g], sc[g + 8]}, sv[2] = {sc[16 + g], sc[24 + g]};
       const int32_t tok = int32_t((first + k * stride) * kTile + g);
       const bool border = tok - int32_t(g) + int32_t(kTile) > all_see;
-      float x[R][4], iv[2];
+      float x[R][4], lv[2];  // S, then the weights
       bool slow = false;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float s = fmaxf(sv[u], 0x1p-100f);  // a zero row: its codes are zero, its weight counts
-        const float lv = lg2(s);
-        iv[u] = rcp(s);
+        lv[u] = lg2(fmaxf(sv[u], 0x1p-149f));  // a row of zeros has codes of zero: any finite logarithm does
         slow |= sv[u] != sv[u];
 #pragma unroll
         for (uint32_t r = 0; r < R; ++r)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float& v = x[r][2 * u + j];
-            v = fmaf(s2[0][r][2 * u + j] + s2[1][r][2 * u + j], sk[u] * rs[r][j], lv);
+            v = (s2[0][r][2 * u + j] + s2[1][r][2 * u + j]) * (sk[u] * rs[r][j]);
             if (border && !(tok + 8 * u < min(lim[r][j], int32_t(len)))) v = -INFINITY;
-            slow |= v > m[r][j] + 15.f;
+            slow |= fmaxf(v - n[r][j], (v + lv[u]) - m[r][j]) > 15.f;
           }
       }
       bool nans = false;  // a value row is NaN
       if (__any_sync(0xffffffffu, slow)) {
         nans = __any_sync(0xffffffffu, sv[0] != sv[0] || sv[1] != sv[1]);
+        // one row's m or n, up to 7 below the largest v of its tokens; the factor that its sums take
+        auto move = [](float& ref, float v0, float v1) {
+          float top = fmaxf(v0, v1);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float to = fmaxf(ref, top - 7.f), f = to == ref ? 1.f : ex2(ref - to);
+          ref = to;
+          return f;
+        };
 #pragma unroll
         for (uint32_t r = 0; r < R; ++r)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(x[r][j], x[r][j + 2]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float to = fmaxf(m[r][j], top - 7.f);
-            const float f = to == m[r][j] ? 1.f : ex2(m[r][j] - to);
-            m[r][j] = to;
-            l[r][j] *= f;
+            l[r][j] *= move(n[r][j], x[r][j], x[r][j + 2]);
+            const float f = move(m[r][j], x[r][j] + lv[0], x[r][j + 2] + lv[1]);
 #pragma unroll
             for (uint32_t i = 0; i < T::kSteps; ++i) {
               o[r][i][j] *= f;
@@ -402,8 +405,8 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const bool hidden = border && x[r][j] == -INFINITY;
-          const float w = hidden ? 0.f : ex2(x[r][j] - m[r][j & 1]);
-          l[r][j & 1] = fmaf(w, iv[j >> 1], l[r][j & 1]);
+          l[r][j & 1] += hidden ? 0.f : ex2(x[r][j] - n[r][j & 1]);
+          const float w = hidden ? 0.f : ex2((x[r][j] + lv[j >> 1]) - m[r][j & 1]);
           x[r][j] = nans && !hidden && sv[j >> 1] != sv[j >> 1] ? sv[j >> 1] : w;
         }
         pw[r][0] = transpose8x8(pack_half(x[r][0], x[r][1]));
@@ -480,14 +483,15 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
         s += __shfl_xor_sync(0xffffffffu, s, 4);
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
-        const float inv = s == 0.f ? 0.f : 1.f / s;
+        // 2^(m - n) in two halves: it may leave fp32's range where the answer does not
+        const float inv = s == 0.f ? 0.f : 1.f / s, half = s == 0.f ? 0.f : exp2f(0.5f * (m[r][j] - n[r][j]));
         const uint32_t row = r * 8 + 2 * t + j;
-        if (g == 0) jl[warp * T::kRows + row] = s == 0.f ? -INFINITY : m[r][j] + log2f(s);
+        if (g == 0) jl[warp * T::kRows + row] = s == 0.f ? -INFINITY : n[r][j] + log2f(s);
         float* dst = jo + (warp * T::kRows + row) * D + g * (D / 8);
 #pragma unroll
         for (uint32_t i = 0; i < T::kSteps; ++i) {
-          dst[2 * i] = o[r][i][j] * inv;
-          dst[2 * i + 1] = o[r][i][j + 2] * inv;
+          dst[2 * i] = o[r][i][j] * inv * half * half;
+          dst[2 * i + 1] = o[r][i][j + 2] * inv * half * half;
         }
       }
     __syncthreads();
