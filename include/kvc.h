@@ -433,7 +433,9 @@ int kvc_cache_write(const kvc_cache* cache, uint32_t dtype, uint32_t n_tokens, c
  * the given dtype (fp32 products s * y rounded to it). Token p of sequence b
  * lies in page d_pages[b * pages_stride + p / page_tokens].
  *   d_start      device [n_seqs]
- *   d_out_start  device [n_seqs + 1], ascending, within [0, out_tokens]
+ *   d_out_start  device [n_seqs + 1], ascending, within [0, out_tokens]; of a
+ *                range that passes the end what fits is read, one that starts
+ *                below zero is not
  * Rows of d_out outside the ranges are left as they are. */
 int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, const int32_t* d_pages,
                    uint32_t pages_stride, const int32_t* d_start, const int32_t* d_out_start, void* d_out,

@@ -189,7 +189,7 @@ __device__ inline int64_t read_row(const CacheView& c, const ReadArgs& a, uint32
     if (__ldg(a.out_start + mid) <= int32_t(t)) lo = mid; else hi = mid - 1;
   }
   const int32_t first = __ldg(a.out_start + lo);
-  if (int32_t(t) < first || int32_t(t) >= __ldg(a.out_start + lo + 1)) return -1;
+  if (int32_t(t) < first || int32_t(t) >= __ldg(a.out_start + lo + 1) || first < 0) return -1;
   const int64_t p = int64_t(__ldg(a.start + lo)) + (int32_t(t) - first);
   const int64_t page_at = p >> c.page_shift;
   if (p < 0 || page_at >= int64_t(a.pages_stride)) {
@@ -269,8 +269,12 @@ __global__ void __launch_bounds__(kThreads) k_cache_read(const CacheView c, cons
   __shared__ int64_t rows[U * kGroups];
   const uint32_t lane = threadIdx.x % L, group = threadIdx.x / L;
   const uint32_t tile = t0 + blockIdx.y * U * kGroups;
-  if (threadIdx.x == 0 && !(blockIdx.x | blockIdx.y) && uint32_t(__ldg(a.out_start + a.n_seqs)) > a.out_tokens)
-    flag_invalid(a.res);  // a range past the end of out
+  // each range is looked at once, whether or not a token of out lies in it
+  const uint64_t id = (uint64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  for (uint64_t b = id; b < a.n_seqs; b += uint64_t(gridDim.x) * gridDim.y * kThreads) {
+    const int32_t first = __ldg(a.out_start + b), last = __ldg(a.out_start + b + 1);
+    if (first < 0 || last < first || last > int32_t(a.out_tokens)) flag_invalid(a.res);
+  }
   for (uint32_t i = threadIdx.x; i < U * kGroups; i += kThreads)
     rows[i] = a.out_tokens - tile > i ? read_row(c, a, tile + i) : -1;
   __syncthreads();
