@@ -268,6 +268,14 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
           make_uint4(w[i].x ^ flip, w[i].y ^ flip, w[i].z ^ flip, w[i].w ^ flip);
     }
     tc::fence_async_smem();
+  } else if (a.q_start) {
+    // each sequence's range and share are looked at once, also where no row lies in
+    // it; with a cache its kernel looks at the ranges
+    const uint64_t id = (uint64_t(blockIdx.y) * gridDim.x + blockIdx.x) * 128u + my;
+    for (uint64_t b = id; b < a.n_seqs; b += uint64_t(gridDim.x) * gridDim.y * 128u) {
+      if (!a.has_cache) rows_of_seq(a, uint32_t(b));
+      prefix_seen(a, uint32_t(b));
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
