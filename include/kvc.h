@@ -397,8 +397,10 @@ int kvc_stage_stream_encode_noalloc(const uint8_t* d_sym, uint32_t n, uint8_t* d
  * Device-side indices (slots, page tables, lengths, starts) are checked on the
  * device: one that is out of range is not followed, and *d_res (which may be
  * NULL) gets status KVC_ERR_INVALID. The calls below write d_res->status in
- * that case only: it stays set until the caller clears it, over any number of
- * calls, so that a captured step can be checked now and then. */
+ * that case, and kvc_attend where a bounded wait gave up (KVC_ERR_TIMEOUT; the
+ * rows concerned get NaN, with or without a d_res), and else never: it stays set
+ * until the caller clears it, over any number of calls, so that a captured step
+ * can be checked now and then. Of several codes the largest stays. */
 enum { KVC_CACHE_E4M3 = 1, KVC_CACHE_INT8 = 2, KVC_CACHE_E2M1 = 3 };
 typedef struct {
   uint32_t format;

@@ -28,7 +28,7 @@
 // pipe's 2048; beginning and end of a block take 19 us.
 //
 // Every wait is bounded: one that runs out sets KVC_ERR_TIMEOUT, stops all roles,
-// and the block leaves after what it has in flight has landed.
+// and the block leaves NaN behind after what it has in flight has landed.
 #pragma once
 #include <cuda.h>
 
@@ -514,7 +514,10 @@ k_attend_prefix(const AttendArgs a, const PartsView parts, const __grid_constant
     if (ok && turns) ok = await(&B.o_done[r], (turns - 1) & 1u);  // the last products
     if (!ok) {
       *stop = 1;
-      if (a.res) *reinterpret_cast<volatile int32_t*>(&a.res->status) = KVC_ERR_TIMEOUT;
+      flag_status(a.res, KVC_ERR_TIMEOUT);
+      // what there is of O is no answer: NaN reaches the output and lse of every row
+      // that needed it, also through the joins
+      l = see ? __uint_as_float(0x7fc00000u) : 0.f;
     }
     tc::fence_after_sync();
     const float inv = l == 0.f ? 0.f : 1.f / l;

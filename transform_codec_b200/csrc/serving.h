@@ -55,10 +55,13 @@ cudaError_t launch_attend(const AttendArgs& a, const CacheView& c, uint32_t max_
 uint64_t attend_ws_bytes(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, bool least);
 
 #ifdef __CUDACC__
-// An index the device refuses to follow: sticky status in the caller's result.
-__device__ inline void flag_invalid(kvc_result* res) {
-  if (res) *reinterpret_cast<volatile int32_t*>(&res->status) = KVC_ERR_INVALID;
+// Sticky status in the caller's result; of two the larger code stays, whichever
+// comes first: KVC_ERR_TIMEOUT before KVC_ERR_INVALID.
+__device__ inline void flag_status(kvc_result* res, int32_t status) {
+  if (res) atomicMax(&res->status, status);
 }
+// An index the device refuses to follow.
+__device__ inline void flag_invalid(kvc_result* res) { flag_status(res, KVC_ERR_INVALID); }
 #endif
 
 }  // namespace kvc
