@@ -450,7 +450,10 @@ int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, cons
  * either of which may be absent (prefix_tokens = 0; cache = NULL), not both.
  * Query heads h * g .. h * g + g - 1 (g = n_q_heads / n_heads) read head h.
  *   dtype          KVC_DTYPE_BF16 or KVC_DTYPE_FP16: q, out and the prefix
- *   n_rows         query tokens that d_q, d_out and d_lse have room for
+ *   n_rows         query tokens that d_q, d_out and d_lse have room for; n_rows *
+ *                  n_q_heads is below 2^31
+ *   n_q_heads, n_seqs   at most 65535
+ *   prefix_tokens, max_kv   below 2^31
  *   head_dim       64 or 128 (else KVC_ERR_UNSUPPORTED)
  *   max_queries, max_kv   expected largest number of queries and of cache tokens
  *                  of a sequence: they size the launch; results do not depend

@@ -236,3 +236,23 @@ def test_binding_refuses_tensors():
         with pytest.raises(kvc.KvcError) as e:
             a.run(kw.pop("q"), kw.pop("out"), **kw)
         assert e.value.status == kvc.ERR_INVALID, n
+
+
+@pytest.mark.parametrize("change", [
+    dict(max_rows=70000, max_seqs=70000), dict(max_rows=-1), dict(max_rows=1 << 26, n_q_heads=64), dict(max_seqs=-1),
+    dict(max_seqs=1 << 16), dict(max_queries=-1), dict(max_queries=1 << 32), dict(max_kv=1 << 31), dict(max_kv=-5),
+    dict(prefix_tokens=1 << 31), dict(prefix_tokens=-1), dict(n_heads=0), dict(n_heads=-2), dict(n_q_heads=1 << 17),
+    dict(n_q_heads=0), dict(max_rows=4.0), dict(max_kv=None),
+])
+def test_binding_refuses_attention_sizes(change):
+    """A size that no call accepts is refused where it is given, not by the first call."""
+    kw = dict(n_q_heads=8, n_heads=2, head_dim=64, max_rows=4, max_seqs=4)
+    with pytest.raises(kvc.KvcError) as e:
+        kvc.Attention(torch.bfloat16, device="cpu", **{**kw, **change})
+    assert e.value.status == kvc.ERR_INVALID
+
+
+def test_binding_accepts_the_largest_attention_sizes():
+    a = kvc.Attention(torch.bfloat16, 8, 2, 64, max_rows=65535, max_seqs=65535, max_kv=1, device="cpu")
+    assert a.workspace.numel() >= 16
+    assert kvc.lib().kvc_attend_workspace_min(a._ref) == 0  # one part a row

@@ -579,7 +579,8 @@ class Attention:
     max_rows query tokens in all, max_seqs sequences, max_queries and max_kv the
     expected most of one sequence, prefix_tokens the longest shared prefix. Runs
     may be smaller; larger ones are refused with ERR_CAPACITY where the
-    workspace does not do."""
+    workspace does not do. At most 65,535 sequences and query heads, and fewer
+    than 2^31 rows times query heads."""
 
     def __init__(self, dtype, n_q_heads: int, n_heads: int, head_dim: int, max_rows: int, max_seqs: int,
                  max_queries: int = 1, max_kv: int = 0, prefix_tokens: int = 0, device=None):
@@ -588,6 +589,13 @@ class Attention:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device, self.dtype = dev, dtype
+        # before they become 32-bit fields; the sizing call answers 0 for what it refuses
+        for v, what in ((n_heads, "n_heads"), (n_q_heads, "n_q_heads"), (head_dim, "head_dim"), (max_rows, "max_rows"),
+                        (max_seqs, "max_seqs"), (max_queries, "max_queries"), (max_kv, "max_kv"),
+                        (prefix_tokens, "prefix_tokens")):
+            _require(isinstance(v, int) and 0 <= v < 1 << 31, f"{what} {v}")
+        _require(n_q_heads <= 65535 and max_seqs <= 65535 and max_rows * n_q_heads < 1 << 31,
+                 f"{n_q_heads} query heads, {max_seqs} sequences, {max_rows} rows")
         d = self._desc = AttendDesc()
         d.dtype, d.n_q_heads, d.n_heads, d.head_dim = _value_type(dtype), n_q_heads, n_heads, head_dim
         d.n_rows, d.n_seqs, d.max_queries, d.max_kv = max_rows, max_seqs, max_queries, max_kv
