@@ -256,3 +256,27 @@ def test_binding_accepts_the_largest_attention_sizes():
     a = kvc.Attention(torch.bfloat16, 8, 2, 64, max_rows=65535, max_seqs=65535, max_kv=1, device="cpu")
     assert a.workspace.numel() >= 16
     assert kvc.lib().kvc_attend_workspace_min(a._ref) == 0  # one part a row
+
+
+@pytest.mark.parametrize("res", [lambda: torch.zeros(2, dtype=torch.int64, device="meta"),
+                                 lambda: torch.zeros(1, dtype=torch.int64), lambda: torch.zeros(3, dtype=torch.int32),
+                                 lambda: torch.zeros(4, dtype=torch.int64)[::2]])
+def test_binding_refuses_results(monkeypatch, res):
+    """A result on another device, or without room for a kvc_result, never reaches the library."""
+    def launched(*args):
+        raise AssertionError("launched")
+    monkeypatch.setattr(kvc, "_launch", launched)
+    c = kvc.QuantCache(kvc.CACHE_INT8, 2, 64, 16, 4, device="cpu")
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    i = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    a = kvc.Attention(torch.bfloat16, 8, 2, 64, 4, 4, max_kv=60, device="cpu")
+    q = torch.zeros(1, 8, 64, dtype=torch.bfloat16)
+    calls = [lambda r: kvc.cache_write(c, k, k, torch.zeros(3, dtype=torch.int64), res=r),
+             lambda r: kvc.cache_read(c, i(0)[None], i(0), i(0, 5), torch.zeros(2, 2, 5, 64), res=r),
+             lambda r: a.run(q, q.clone(), cache=c, page_table=i(0)[None], kv_len=i(1), res=r)]
+    for call in calls:
+        with pytest.raises(kvc.KvcError) as e:
+            call(res())
+        assert e.value.status == kvc.ERR_INVALID
+        with pytest.raises(AssertionError):  # a good one does
+            call(torch.zeros(2, dtype=torch.int64))

@@ -462,6 +462,13 @@ def _on(t, device, what: str, dtype):
         _refuse(f"{what}: {t.dtype} on {t.device}, not {dtype} on {device}")
 
 
+def _result(res, device) -> int:
+    """The address of a caller's kvc_result: 16 bytes on the tensors' device."""
+    if res.device != device or res.numel() * res.element_size() < 16 or not res.is_contiguous():
+        _refuse(f"res: {tuple(res.shape)} {res.dtype} on {res.device}")
+    return res.data_ptr()
+
+
 def _launch(device, stream, what: str, fn, *args):
     """fn(*args, stream) with the tensors' device current, on its current stream if none is given."""
     torch = _use_torch()
@@ -543,7 +550,8 @@ def cache_write(cache: QuantCache, k, v, slots, res=None, stream=None):
     if kc != 1 or vc != 1 or not slots.is_contiguous():
         _refuse("channels and slots are contiguous")
     _launch(device, stream, "kvc_cache_write", _lib.kvc_cache_write, cache.ref, _value_type(dtype), shape[0],
-            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(), cache._res if res is None else res.data_ptr())
+            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slots.data_ptr(),
+            cache._res if res is None else _result(res, device))
 
 
 def cache_read(cache: QuantCache, page_table, start, out_start, out, res=None, stream=None):
@@ -568,7 +576,7 @@ def cache_read(cache: QuantCache, page_table, start, out_start, out, res=None, s
         _refuse("contiguous tensors")
     _launch(device, stream, "kvc_cache_read", _lib.kvc_cache_read, cache.ref, _value_type(out.dtype), n,
             page_table.data_ptr(), page_table.shape[1], start.data_ptr(), out_start.data_ptr(), out.data_ptr(),
-            out.shape[2], cache._res if res is None else res.data_ptr())
+            out.shape[2], cache._res if res is None else _result(res, device))
 
 
 class Attention:
@@ -688,7 +696,7 @@ class Attention:
             d.prefix_tokens, d.prefix_head_stride = pk.shape[1], st[0]
             d.prefix_k, d.prefix_v = pk.data_ptr(), pv.data_ptr()
         _launch(dev, stream, "kvc_attend", _lib.kvc_attend, self._ref, self._ws, self._ws_bytes,
-                self._res if res is None else res.data_ptr())
+                self._res if res is None else _result(res, dev))
 
     def _sequences(self, t, what, extra, seqs):
         """The number of sequences that t speaks of, the same as what was said before (-1: nothing yet)."""
