@@ -478,7 +478,8 @@ int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, cons
  *                  times it). Keys, and everything behind the longest share, may
  *                  hold anything.
  * A row that sees nothing gets zeros and lse = -infinity. Rows outside
- * [d_q_start[0], d_q_start[n_seqs]) are left as they are.
+ * [d_q_start[0], d_q_start[n_seqs]) are left as they are. With n_rows or n_seqs
+ * of 0 nothing is done, and the device pointers are not looked at.
  * kvc_attend_workspace_bytes is the workspace at which the work is split best;
  * kvc_attend takes any size from kvc_attend_workspace_min up (0 when one part
  * covers each row) and returns KVC_ERR_CAPACITY below it. d_ws is 16-byte

@@ -60,3 +60,21 @@ def test_attention_reports_bad_shares_of_sequences_without_rows(with_cache, shar
     assert kvc.read_result(att.res)[0] == kvc.OK
     att.run(q, out, prefix=prefix, q_start=i32(starts), prefix_len=i32(share), **kw)
     assert kvc.read_result(att.res)[0] == kvc.ERR_INVALID
+
+
+def test_empty_steps():
+    """No rows, and sequences without any: nothing is written and nothing refused."""
+    host = HostCache(kvc.CACHE_INT8, 1, 64, 16, [40], seed=2)
+    c = host.gpu()
+    prefix = tuple(_randn(s, 1, 200, 64, dt=torch.bfloat16).cuda() for s in (1, 2))
+    att = kvc.Attention(torch.bfloat16, 4, 1, 64, max_rows=2, max_seqs=2, max_kv=40, prefix_tokens=200)
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros(0, 3, dtype=torch.int32, device="cuda"), i32([])
+    for kw in (dict(cache=c, page_table=table, kv_len=lens), dict(prefix=prefix), dict(prefix=prefix, prefix_len=lens),
+               dict(cache=c, page_table=table, kv_len=lens, prefix=prefix, q_start=i32([0])),
+               dict(cache=c, page_table=host.table.cuda(), kv_len=i32([40]), q_start=i32([0, 0]))):
+        att.run(q, q.clone(), lse=torch.zeros(0, 4, device="cuda"), **kw)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 5.0)
+    att.run(q, out, cache=c, page_table=table, kv_len=lens, q_start=i32([0]))
+    assert (out == 5.0).all() and kvc.read_result(att.res)[0] == kvc.OK

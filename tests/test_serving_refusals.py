@@ -280,3 +280,26 @@ def test_binding_refuses_results(monkeypatch, res):
         assert e.value.status == kvc.ERR_INVALID
         with pytest.raises(AssertionError):  # a good one does
             call(torch.zeros(2, dtype=torch.int64))
+
+
+EMPTY = r'''
+none = dict(q=None, out=None, lse=None, pages=None, kv_len=None, prefix_k=None, prefix_v=None, prefix_len=None)
+attend("no rows", n_rows=0, n_seqs=0, q_start=None, c=cache(codes=None, scales=None, micro=None), **none)
+attend("no sequences", n_seqs=0, **dict(none, q=A, out=A, lse=A))
+attend("sequences without rows", n_rows=0, **none)
+attend("no prefix", n_rows=0, n_seqs=0, prefix_tokens=0, ws=None, ws_bytes=0, **none)
+'''
+EMPTY_BAD = r'''
+attend("shape", n_rows=0, n_seqs=0, n_q_heads=7)
+attend("cache shape", n_rows=0, n_seqs=0, c=cache(page_tokens=24))
+attend("a sequence without a row", n_rows=0, n_seqs=1, q_start=None)
+attend("nothing to see", n_rows=0, n_seqs=0, cache=None, prefix_tokens=0)
+'''
+
+
+def test_empty_attention_needs_no_arrays():
+    """Empty tensors have no address; shapes are looked at all the same."""
+    got = _calls(EMPTY)
+    assert {v for k, v in got.items() if k.startswith("attend")} == {kvc.OK}, got
+    got = _calls(EMPTY_BAD)
+    assert {v for k, v in got.items() if k.startswith("attend")} == {kvc.ERR_INVALID}, got

@@ -75,8 +75,6 @@ int attend_args(const kvc_attend_desc* d, AttendArgs& a, CacheView& cv, bool poi
         !stride_ok(d->out_token_stride, vb) || !stride_ok(d->out_head_stride, vb))
       return KVC_ERR_INVALID;
     if (d->cache && (!d->d_pages || !d->d_kv_len || !d->pages_stride)) return KVC_ERR_INVALID;
-    // without d_q_start sequence b is row b
-    if (!d->d_q_start && d->n_rows < d->n_seqs) return KVC_ERR_INVALID;
     if (d->prefix_tokens) {
       if (!d->d_prefix_k || !d->d_prefix_v || !aligned16(d->d_prefix_k) || !aligned16(d->d_prefix_v))
         return KVC_ERR_INVALID;
@@ -184,14 +182,17 @@ extern "C" int kvc_attend(const kvc_attend_desc* desc, void* d_ws, size_t ws_byt
                           cudaStream_t stream) {
   AttendArgs a;
   CacheView c;
-  const int st = attend_args(desc, a, c, true);
+  // a step without rows or sequences has empty arrays, whose addresses may be NULL
+  const bool work = desc && desc->n_rows && desc->n_seqs;
+  const int st = attend_args(desc, a, c, work);
   if (st != KVC_OK) return st;
+  if (!desc->d_q_start && desc->n_rows < desc->n_seqs) return KVC_ERR_INVALID;  // sequence b is row b
   if (!aligned16(d_ws) || (reinterpret_cast<uintptr_t>(d_res) & 7u)) return KVC_ERR_INVALID;
   const uintptr_t words = reinterpret_cast<uintptr_t>(a.lse) | reinterpret_cast<uintptr_t>(a.q_start) |
                           reinterpret_cast<uintptr_t>(a.pages) | reinterpret_cast<uintptr_t>(a.kv_len) |
                           reinterpret_cast<uintptr_t>(a.prefix_len);
   if (words & 3u) return KVC_ERR_INVALID;
-  if (!a.n_rows || !a.n_seqs) return KVC_OK;
+  if (!work) return KVC_OK;
   if (!d_ws) ws_bytes = 0;
   if (ws_bytes < attend_ws_bytes(a, desc->max_queries, desc->max_kv, true)) return KVC_ERR_CAPACITY;
   a.res = d_res;
