@@ -457,7 +457,9 @@ int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, cons
  *   head_dim       64 or 128 (else KVC_ERR_UNSUPPORTED)
  *   max_queries, max_kv   expected largest number of queries and of cache tokens
  *                  of a sequence: they size the launch; results do not depend
- *                  on their being right
+ *                  on their being right, but a max_kv far too small leaves a long
+ *                  sequence to few blocks. max_kv = 0: not known, split as for a
+ *                  long one within a workspace of 32 MB
  *   d_q, d_out     device; head h of token t at t * token stride + h * head stride
  *                  (in values), channels contiguous; 16-byte aligned, strides
  *                  multiples of 16 bytes

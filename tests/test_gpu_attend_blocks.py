@@ -104,3 +104,22 @@ def test_join_of_more_than_256_parts(dim, group, queries):
         want, wl, tol = attention(q, [0, queries], host, p, None, dim ** -0.5)
         check_out(out, lse, want, wl, tol)
         assert kvc.read_result(att.res) == (kvc.OK, 0)
+
+
+@pytest.mark.parametrize("queries", [1, 3])
+def test_a_length_that_is_not_known(queries):
+    """No max_kv given: long and short sequences, with and without a prefix."""
+    lens = [9001, 5, 0]
+    host = HostCache(kvc.CACHE_E4M3, 2, 128, 64, lens, seed=5)
+    q = _randn(6, 3 * queries, 16, 128, dt=torch.bfloat16, spread=1.0)
+    starts = [0, queries, 2 * queries, 3 * queries]
+    prefix = tuple(_randn(s, 2, 200, 128, dt=torch.bfloat16) for s in (1, 2))
+    for p in (None, prefix):
+        att = kvc.Attention(q.dtype, 16, 2, 128, max_rows=3 * queries, max_seqs=3, max_queries=queries,
+                            prefix_tokens=200 if p else 0)
+        out = torch.zeros(3 * queries, 16, 128, dtype=q.dtype, device="cuda")
+        lse = torch.zeros(3 * queries, 16, device="cuda")
+        att.run(q.cuda(), out, cache=host.gpu(), page_table=host.table.cuda(), kv_len=i32(lens), lse=lse,
+                q_start=i32(starts), prefix=tuple(x.cuda() for x in p) if p else None)
+        want, wl, tol = attention(q, starts, host, p, None, 128 ** -0.5)
+        check_out(out, lse, want, wl, tol)

@@ -303,3 +303,20 @@ def test_empty_attention_needs_no_arrays():
     assert {v for k, v in got.items() if k.startswith("attend")} == {kvc.OK}, got
     got = _calls(EMPTY_BAD)
     assert {v for k, v in got.items() if k.startswith("attend")} == {kvc.ERR_INVALID}, got
+
+
+def _workspace(**kw):
+    d = dict(n_q_heads=64, n_heads=8, head_dim=128, max_rows=1, max_seqs=1, device="cpu")
+    return kvc.Attention(torch.bfloat16, **{**d, **kw}).workspace.numel()
+
+
+def test_a_length_that_is_not_known_is_split_like_a_long_one():
+    """One query of 64 heads: the same parts as for 131,072 tokens. The workspace is bounded, and a prefix keeps its
+    own parts."""
+    assert _workspace() == _workspace(max_kv=131072) > 64 * 64 * 129 * 4
+    assert _workspace(max_kv=1) == 16
+    for rows, seqs in ((64, 1), (64, 64), (4096, 1), (65535, 65535)):
+        prefix = _workspace(max_rows=rows, max_seqs=seqs, prefix_tokens=8192, max_kv=1)
+        both = _workspace(max_rows=rows, max_seqs=seqs, prefix_tokens=8192)
+        one = rows * 64 * 129 * 4
+        assert prefix <= both <= prefix + max(32 << 20, one)

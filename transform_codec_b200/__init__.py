@@ -585,7 +585,7 @@ class Attention:
 
     dtype (torch.bfloat16 or torch.float16) is that of q, out and the prefix;
     max_rows query tokens in all, max_seqs sequences, max_queries and max_kv the
-    expected most of one sequence, prefix_tokens the longest shared prefix. Runs
+    expected most of one sequence (max_kv 0: not known), prefix_tokens the longest shared prefix. Runs
     may be smaller; larger ones are refused with ERR_CAPACITY where the
     workspace does not do. At most 65,535 sequences and query heads, and fewer
     than 2^31 rows times query heads."""

@@ -142,6 +142,11 @@ uint64_t parts_bytes(const AttendArgs& a, uint64_t parts) {
   return (parts * rows * sizeof(float) + 15) / 16 * 16 + parts * rows * a.D * sizeof(float);
 }
 
+// Parts of the cache's tokens where the longest sequence is not known: as many as a
+// long one takes, within this many bytes of results (one query over 64 heads of 128
+// takes 74 parts, 2.4 MB; rows that pass it fill the SMs by themselves).
+constexpr uint64_t kUnknownBytes = 32u << 20;
+
 // most: parts that the workspace has room for
 Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint64_t most) {
   Division d{1, 1, 1, 0, 0, 1};
@@ -175,6 +180,8 @@ Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint
     // One sequence: as many parts as fill the SMs once (4 or 3 blocks each), of at
     // least 64 tokens. A batch: the same, or parts of about 512 tokens until there
     // are some four waves of blocks, so that different lengths even out.
+    const bool known = max_kv != 0;
+    if (!known) max_kv = 0x7fffffffu;
     const uint64_t wave = kSMs * (d.row_tiles == 1 ? 4 : 3), blocks = uint64_t(a.n_seqs) * a.H * d.row_groups;
     const uint64_t fine = std::max<uint64_t>(1, (uint64_t(max_kv) + kLeastTiles * kTile - 1) / (kLeastTiles * kTile));
     uint64_t s = std::min(fine, std::max<uint64_t>(1, wave / std::max<uint64_t>(blocks, 1)));
@@ -182,7 +189,8 @@ Division divide(const AttendArgs& a, uint32_t max_queries, uint32_t max_kv, uint
       const uint64_t coarse = std::max<uint64_t>(1, uint64_t(max_kv) / 512);
       s = std::max(s, std::min(coarse, std::max<uint64_t>(1, 4 * wave / std::max<uint64_t>(blocks, 1))));
     }
-    s = std::min<uint64_t>(s, 512);
+    if (!known) s = std::min(s, kUnknownBytes / (std::max<uint64_t>(a.n_rows, 1) * a.Hq * (a.D + 1) * sizeof(float)));
+    s = std::max<uint64_t>(1, std::min<uint64_t>(s, 512));
     if (s + d.prefix_parts > 1 && s + d.prefix_parts > most) s = most > d.prefix_parts + 1 ? most - d.prefix_parts : 1;
     d.splits = uint32_t(s);
   }
