@@ -449,7 +449,16 @@ int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, cons
  *   - each sequence's own tokens in a quantised cache,
  * either of which may be absent (prefix_tokens = 0; cache = NULL), not both.
  * Query heads h * g .. h * g + g - 1 (g = n_q_heads / n_heads) read head h.
- *   dtype          KVC_DTYPE_BF16 or KVC_DTYPE_FP16: q, out and the prefix
+ *   dtype          KVC_DTYPE_BF16 or KVC_DTYPE_FP16: q, out and the prefix. Scores,
+ *                  sums and outputs are fp32 until the output is rounded once. In
+ *                  16 bits are the weights: of the prefix in the dtype (the sum
+ *                  of weights takes them unrounded), of the cache in fp16 after
+ *                  multiplication by the token's value scale, none off by more
+ *                  than half a step of itself or 2^-32 of the row's largest; and
+ *                  for the cache a query's elements, exact or off by 2^-32 of
+ *                  its largest. Exponentials and logarithms are approximations
+ *                  to about 2^-18 of a weight, 2^-15 where value scales lie near
+ *                  the ends of the range
  *   n_rows         query tokens that d_q, d_out and d_lse have room for; n_rows *
  *                  n_q_heads is below 2^31
  *   n_q_heads, n_seqs   at most 65535
@@ -477,8 +486,9 @@ int kvc_cache_read(const kvc_cache* cache, uint32_t dtype, uint32_t n_seqs, cons
  *                  sees; NULL: all
  *                  Prefix values are finite up to the longest share: one that is
  *                  not may reach rows that do not see its token (a weight of zero
- *                  times it). Keys, and everything behind the longest share, may
- *                  hold anything.
+ *                  times it). They are below 2^80 (bf16), so that their sums with
+ *                  weights of up to 2^15 stay within fp32. Keys, and everything
+ *                  behind the longest share, may hold anything.
  * A row that sees nothing gets zeros and lse = -infinity. Rows outside
  * [d_q_start[0], d_q_start[n_seqs]) are left as they are. With n_rows or n_seqs
  * of 0 nothing is done, and the device pointers are not looked at.

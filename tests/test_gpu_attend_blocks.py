@@ -123,3 +123,14 @@ def test_a_length_that_is_not_known(queries):
                 q_start=i32(starts), prefix=tuple(x.cuda() for x in p) if p else None)
         want, wl, tol = attention(q, starts, host, p, None, 128 ** -0.5)
         check_out(out, lse, want, wl, tol)
+
+
+def test_large_prefix_values():
+    """Values of 2^79 under weights that stay far above the reference: sums of P V within fp32."""
+    tokens = 40000
+    prefix = [_randn(s, 1, tokens, 64, dt=torch.bfloat16) for s in (1, 2)]
+    prefix[1] = (prefix[1].float().clamp(-0.99, 0.99) * 2.0 ** 79).bfloat16()
+    prefix[0][:] = 0
+    prefix[0][:, 128:, 0] = 64 * 0.6931471805599453 / 8  # scores of 2^8 the first block's
+    q = torch.ones(2, 4, 64, dtype=torch.bfloat16)
+    _run(q, [0, 1, 2], prefix, [tokens, tokens - 77])

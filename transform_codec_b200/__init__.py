@@ -585,10 +585,10 @@ class Attention:
 
     dtype (torch.bfloat16 or torch.float16) is that of q, out and the prefix;
     max_rows query tokens in all, max_seqs sequences, max_queries and max_kv the
-    expected most of one sequence (max_kv 0: not known), prefix_tokens the longest shared prefix. Runs
-    may be smaller; larger ones are refused with ERR_CAPACITY where the
-    workspace does not do. At most 65,535 sequences and query heads, and fewer
-    than 2^31 rows times query heads."""
+    expected most of one sequence (max_kv 0: not known), prefix_tokens the
+    longest shared prefix. Runs may be smaller; larger ones are refused with
+    ERR_CAPACITY where the workspace does not do. At most 65,535 sequences and
+    query heads, and fewer than 2^31 rows times query heads."""
 
     def __init__(self, dtype, n_q_heads: int, n_heads: int, head_dim: int, max_rows: int, max_seqs: int,
                  max_queries: int = 1, max_kv: int = 0, prefix_tokens: int = 0, device=None):
