@@ -17,9 +17,8 @@
 // so that a token's share of it does not depend on how large its values are: a
 // row of zeros beside rows of 2^100 counts like any other. (Summing w / s_v saves
 // that exponential, 3 to 5% of the time, and loses tokens whose scale is 2^-126 of
-// the largest.) m and n move only
-// when passed by 15 (weights up to 2^15 are as exact), so the usual tile needs no
-// exchange between lanes but one vote.
+// the largest.) m and n move only when passed by 15 (weights up to 2^15 are as
+// exact), so the usual tile needs no exchange between lanes but one vote.
 //
 // Layout: the order of channels within the first product and of tokens within
 // the second is free, and is chosen such that a thread's own fragments are
@@ -31,10 +30,13 @@
 // Each warp takes tiles of the block's part with a softmax of its own; the four are
 // joined at the end.
 //
-// Measured: 131,072 tokens of 8 heads x 128 in int8 for one query, 277 MB, 61 us (4.5
-// TB/s; 42 us at the measured 6.56; the loads alone take 58). 4-bit codes are bound
-// by instructions: 411 a tile and warp, 61% of issue slots, 64 sequences with 321 MB
-// in 93 us. With more than 16 query rows a sequence each 16 take the codes again.
+// Measured: 131,072 tokens of 8 heads x 128 in int8 for one query, 277 MB, 72 us for
+// the call (42 us at the measured 6.56 TB/s); the kernel issues 452 instructions a
+// tile and warp, half of its slots. 64 sequences of up to 8192 tokens on 4-bit pages,
+// 321 MB, 106 us (49): 464 a tile, 68% of the slots of SMs that run, and SMs stand
+// still for 17% of the launch, since sequences of different lengths are cut into the
+// same number of parts. With more than 16 query rows a sequence each 16 take the
+// codes again: 32 sequences of 32,768 tokens, up to 4 queries of 8 heads, 731 us (332).
 #pragma once
 #include <type_traits>
 

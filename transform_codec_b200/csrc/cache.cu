@@ -3,12 +3,13 @@
 // Both move each value once: a bf16 row of 128 channels is 256 bytes on one side
 // and 132 (8-bit) or 76 (4-bit, micro-scales included) on the other. Reading is
 // bound by memory (eight sequences of e4m3 to bf16, 281 MB, 45 us: 6.2 TB/s of 6.56
-// measured). Writing 4-bit rows is bound by instructions, two reciprocals and the
-// conversions above all (30,247 tokens of 2 x 8 x 128, 165 MB, 43 us: 78% of issue
-// slots). A row (token, key/value, head) belongs to a group of
-// lanes, 8 values a lane, so a row is read and written in whole 32-byte
-// sectors, its magnitude is a few shuffles, and every thread has several rows'
-// loads in flight. Consecutive blocks take the 2 * H heads of the same tokens:
+// measured). Writing is bound by instructions: 30,247 tokens of 2 x 8 x 128 take 43
+// to 46 us in 4 bits (165 MB, 25 us at 6.56; 140 warp instructions for each two rows,
+// two reciprocals and the conversions above all; 78% of issue slots at 1.88 GHz), 40
+// in e4m3 and 45 in int8 (188 MB, 29 us; e4m3 106 instructions, 73%). A row (token,
+// key/value, head) belongs to a group of lanes, 8 values a lane, so a row is read and
+// written in whole 32-byte sectors, its magnitude is a few shuffles, and every
+// thread has several rows' loads in flight. Consecutive blocks take the 2 * H heads of the same tokens:
 // they touch neighbouring memory on the token-major side at the same time.
 #include "cache_codes.cuh"
 #include "serving.h"
