@@ -105,3 +105,34 @@ def test_sum_of_many_zero_rows():
     want, wl, tol = attention(q, [0, 1], host, scale=1.0)
     check_out(out, lse, want, wl, tol)
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("gap", [100, 128, 140])
+def test_large_values_far_below_the_largest_score(fmt, gap):
+    """Zero rows with scores 2^gap of the others', in parts and warps of their own, beside rows of 1e30: what the
+    others weigh is below fp32's range and their share of the answer is not."""
+    dim = 128
+    for n, prefix_rows in ((70, 0), (2000, 0), (70, 200)):
+        host = HostCache(FORMATS[fmt], 1, dim, 16, [n], seed=4)
+        _set_values(host, 0, torch.cat((torch.zeros(1, 16, dim), _randn(5, 1, n - 16, dim) * 1e30), 1))
+        pos = torch.arange(n)
+        page, at = host.table[0].long()[pos // 16], pos % 16
+        keys = torch.full((n, 1, dim), 0.0)
+        keys[:16] = 1.0
+        kc, ks, km = quantise(host.fmt, keys)
+        host.codes[page, 0, :, at], host.scales[page, 0, :, at] = kc, ks
+        if km is not None:
+            host.micro[page, 0, :, at] = km
+        prefix = None
+        if prefix_rows:
+            prefix = (torch.zeros(1, prefix_rows, dim).bfloat16(), _randn(6, 1, prefix_rows, dim, dt=torch.bfloat16))
+        q = torch.ones(1, 8, dim, dtype=torch.bfloat16)
+        scale = gap * 0.6931471805599453 / dim
+        att = kvc.Attention(q.dtype, 8, 1, dim, max_rows=1, max_seqs=1, max_kv=n, prefix_tokens=prefix_rows)
+        out, lse = torch.zeros(1, 8, dim, dtype=q.dtype, device="cuda"), torch.zeros(1, 8, device="cuda")
+        att.run(q.cuda(), out, cache=host.gpu(), page_table=host.table.cuda(), kv_len=i32([n]), lse=lse, scale=scale,
+                prefix=None if prefix is None else tuple(p.cuda() for p in prefix))
+        want, wl, (tol, ltol) = attention(q, [0, 1], host, prefix, None, scale)
+        assert want.abs().max() > 1e-14
+        check_out(out, lse, want, wl, (tol * (1 + 2.0 ** -6.9), ltol))

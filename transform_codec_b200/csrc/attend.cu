@@ -71,13 +71,13 @@ k_attend_join(const AttendArgs a, const CacheView c, const PartsView parts, cons
   float sum = 0.f, y[kPer];
 #pragma unroll
   for (uint32_t j = 0; j < kPer; ++j) y[j] = 0.f;
-  // this warp's parts: part0, part0 + kWarps, ..; 32 weights at a time, one a lane
+  // this warp's parts: part0, part0 + kWarps, ..; 32 half factors at a time, one a lane
   for (uint32_t p0 = part0; p0 < n; p0 += 32 * kWarps) {
     float f = 0.f;
     const uint32_t mine = p0 + lane * kWarps;
     if (mine < n) {
       const float L = lse[mine * parts.rows];
-      f = L == -INFINITY ? 0.f : ex2(L - top);
+      f = L == -INFINITY ? 0.f : ex2(0.5f * (L - top));
     }
     const uint32_t here = min(32u, (n - p0 + kWarps - 1) / kWarps);
     for (uint32_t q = 0; q < here; q += 4) {
@@ -102,9 +102,9 @@ k_attend_join(const AttendArgs a, const CacheView c, const PartsView parts, cons
       }
 #pragma unroll
       for (uint32_t u = 0; u < 4; ++u) {
-        sum += w[u];
+        sum = fmaf(w[u], w[u], sum);
 #pragma unroll
-        for (uint32_t j = 0; j < kPer; ++j) y[j] = fmaf(w[u], v[u][j], y[j]);
+        for (uint32_t j = 0; j < kPer; ++j) y[j] = fmaf(w[u], w[u] * v[u][j], y[j]);
       }
     }
   }

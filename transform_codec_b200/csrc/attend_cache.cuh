@@ -509,11 +509,11 @@ k_attend_cache(const AttendArgs a, const CacheView c, const PartsView parts, con
       for (uint32_t j = 0; j < kPer; ++j) y[j] = 0.f;
 #pragma unroll
       for (uint32_t i = 0; i < T::kWarps; ++i) {
-        const float f = w[i] == -INFINITY ? 0.f : ex2(w[i] - top);
-        sum += f;
+        const float f = w[i] == -INFINITY ? 0.f : ex2(0.5f * (w[i] - top));  // half the factor
+        sum = fmaf(f, f, sum);
 #pragma unroll
         for (uint32_t j = 0; j < kPer; ++j)
-          y[j] = fmaf(f, jo[(i * T::kRows + row) * D + lane * kPer + j], y[j]);
+          y[j] = fmaf(f, f * jo[(i * T::kRows + row) * D + lane * kPer + j], y[j]);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll

@@ -4,7 +4,9 @@
 // A part is attention over some of a row's tokens: the normalised output in
 // fp32 and the base-2 logarithm of its sum of exponentials, L. Parts join as
 // sum_p 2^(L_p - L) o_p with L = log2 sum_p 2^L_p; one that saw nothing has L =
-// -infinity and o = 0.
+// -infinity and o = 0. The factors are multiplied in as two halves, 2^((L_p - L) / 2):
+// one below fp32's range may stand before values far above 1 (a part of zero rows
+// with large scores beside one of rows of 2^100).
 #pragma once
 #include "cache_codes.cuh"
 #include "serving.h"
