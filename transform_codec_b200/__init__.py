@@ -632,7 +632,8 @@ class Attention:
         """q, out [n, n_q_heads, head_dim] (token and head strides free in 16-byte
         steps); cache with page_table int32 [n_seqs, pages] and kv_len int32
         [n_seqs]; q_start int32 [n_seqs + 1] (None: one query a sequence); prefix
-        (k, v), each [n_heads, tokens, head_dim], tokens contiguous; prefix_len
+        (k, v), each [n_heads, tokens, head_dim], tokens contiguous, v finite up to
+        the longest share and below 2^80 in magnitude (kvc.h); prefix_len
         int32 [n_seqs] (None: all of it); lse fp32 [n, n_q_heads]; scale defaults
         to head_dim ** -0.5."""
         torch = _torch
